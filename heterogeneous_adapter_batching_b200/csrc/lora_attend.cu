@@ -1,0 +1,168 @@
+// Attention, plain: one CTA per (query row, query head), its warps stride over
+// the keys with a running maximum and sum each, and are joined at the end.
+#include "lora_internal.cuh"
+#include "lora_kv.cuh"
+
+namespace lora {
+namespace {
+
+constexpr int kWarps = 4;
+
+template <class H>
+__device__ __forceinline__ float to_f(H x) { return (float)x; }
+
+// Keys and values of a request from the cache.
+template <int DIM>
+struct CachedKv {
+    KvCache c;
+    const int32_t *table;
+    int h;
+    int32_t *err;
+    __device__ __forceinline__ bool at(int j, float (&k)[DIM / 32], float (&v)[DIM / 32]) const {
+        const int page = table[j / c.block], off = j % c.block, lane = threadIdx.x & 31;
+        if (page < 0 || page >= c.num_pages) {
+            if (err && lane == 0) atomicOr(err, LORA_DEV_ERR_BAD_PAGE);
+            return false;
+        }
+        const unsigned char *g = c.pages + page * c.page_bytes +
+                                 (long long)(h * c.granules + off / LORA_KV_GRANULE) * kv_granule_bytes(DIM);
+        const int row = off % LORA_KV_GRANULE;
+#pragma unroll
+        for (int i = 0; i < DIM / 32; ++i) {
+            const int d = lane * (DIM / 32) + i;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const unsigned char *p = g + w * kv_half_bytes(DIM);
+                const int b = p[row * (DIM / 2) + d / 2];
+                const float2 s = __half22float2(
+                    reinterpret_cast<const __half2 *>(p + kv_code_bytes(DIM))[row * (DIM / LORA_KV_GROUP) + d / LORA_KV_GROUP]);
+                (w ? v : k)[i] = fmaf((float)((d & 1) ? b >> 4 : b & 15), s.x, s.y);
+            }
+        }
+        return true;
+    }
+};
+
+template <int DIM, class H>
+struct DenseKv {
+    const H *kp, *vp;
+    long long kts, vts;
+    __device__ __forceinline__ bool at(int j, float (&k)[DIM / 32], float (&v)[DIM / 32]) const {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < DIM / 32; ++i) {
+            k[i] = (float)kp[j * kts + lane * (DIM / 32) + i];
+            v[i] = (float)vp[j * vts + lane * (DIM / 32) + i];
+        }
+        return true;
+    }
+};
+
+template <int DIM, class H, class Kv>
+__device__ __forceinline__ void attend_row(const Kv &kv, int n, const H *q, H *o, float *lse, float scale) {
+    constexpr int E = DIM / 32;
+    __shared__ float sm_m[kWarps], sm_l[kWarps], sm_o[kWarps][DIM];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float qv[E], acc[E] = {}, m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) qv[i] = to_f(q[lane * E + i]) * scale;
+    for (int j = warp; j < n; j += kWarps) {
+        float k[E], v[E], s = 0.f;
+        if (!kv.at(j, k, v)) continue;
+#pragma unroll
+        for (int i = 0; i < E; ++i) s = fmaf(qv[i], k[i], s);
+        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+        const float mn = fmaxf(m, s), f = m == -INFINITY ? 0.f : __expf(m - mn), p = mn == -INFINITY ? 0.f : __expf(s - mn);
+        l = l * f + p;
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = acc[i] * f + (p > 0.f || p != p ? p * v[i] : 0.f);
+        m = mn;
+    }
+    if (lane == 0) {
+        sm_m[warp] = m;
+        sm_l[warp] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) sm_o[warp][lane * E + i] = acc[i];
+    __syncthreads();
+    float mm = -INFINITY, ll = 0.f;
+    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w]);
+    for (int w = 0; w < kWarps; ++w) ll += sm_m[w] == -INFINITY ? 0.f : sm_l[w] * __expf(sm_m[w] - mm);
+    for (int d = threadIdx.x; d < DIM; d += kWarps * 32) {
+        float s = 0.f;
+        for (int w = 0; w < kWarps; ++w) s += sm_m[w] == -INFINITY ? 0.f : sm_o[w][d] * __expf(sm_m[w] - mm);
+        o[d] = (H)(mm == -INFINITY ? 0.f : s / ll);
+    }
+    if (lse && threadIdx.x == 0) *lse = mm == -INFINITY ? -INFINITY : mm + logf(ll);
+}
+
+// First request whose rows end after t (R: none).
+__device__ __forceinline__ int request_of(const int32_t *cu, int R, int t) {
+    int lo = 0, hi = R;
+    while (lo < hi) {
+        const int m = (lo + hi) >> 1;
+        if (cu[m + 1] > t) hi = m;
+        else lo = m + 1;
+    }
+    return lo;
+}
+
+template <int DIM, class H>
+__global__ void __launch_bounds__(kWarps * 32) attend_cached_kernel(AttendArgs a) {
+    const int t = blockIdx.x, hq = blockIdx.y;
+    const int r = request_of(a.cu_q, a.R, t);
+    if (r >= a.R || t < a.cu_q[r]) return;
+    const int q0 = a.cu_q[r], n = a.cu_q[r + 1] - q0, len = a.kv_len[r];
+    if (n > a.max_q || len < 0 || (long long)len > (long long)a.max_blocks * a.c.block) {
+        if (a.err && threadIdx.x == 0) atomicOr(a.err, LORA_DEV_ERR_BAD_LENGTH);
+        return;
+    }
+    const CachedKv<DIM> kv{a.c, a.table + (size_t)r * a.max_blocks, hq / (a.hq / a.c.heads), a.err};
+    attend_row<DIM, H>(kv, len - n + (t - q0) + 1, reinterpret_cast<const H *>(a.q.p) + t * a.q.ts + hq * a.q.hs,
+                       reinterpret_cast<H *>(a.o.p) + t * a.o.ts + hq * a.o.hs,
+                       a.lse ? a.lse + (size_t)t * a.hq + hq : nullptr, a.scale);
+}
+
+template <int DIM, class H>
+__global__ void __launch_bounds__(kWarps * 32) attend_prompt_kernel(PromptArgs a) {
+    const int t = blockIdx.x, hq = blockIdx.y, h = hq / (a.hq / a.hkv);
+    const int r = request_of(a.cu_q, a.R, t);
+    if (r >= a.R || t < a.cu_q[r]) return;
+    const int q0 = a.cu_q[r], q1 = a.cu_q[r + 1], k0 = a.cu_k[r], k1 = a.cu_k[r + 1];
+    if (q0 < 0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk) {
+        if (a.err && threadIdx.x == 0) atomicOr(a.err, LORA_DEV_ERR_BAD_LENGTH);
+        return;
+    }
+    const DenseKv<DIM, H> kv{reinterpret_cast<const H *>(a.k.p) + k0 * a.k.ts + h * a.k.hs,
+                             reinterpret_cast<const H *>(a.v.p) + k0 * a.v.ts + h * a.v.hs, a.k.ts, a.v.ts};
+    attend_row<DIM, H>(kv, (k1 - k0) - (q1 - q0) + (t - q0) + 1,
+                       reinterpret_cast<const H *>(a.q.p) + t * a.q.ts + hq * a.q.hs,
+                       reinterpret_cast<H *>(a.o.p) + t * a.o.ts + hq * a.o.hs,
+                       a.lse ? a.lse + (size_t)t * a.hq + hq : nullptr, a.scale);
+}
+
+}  // namespace
+
+size_t attend_workspace(int, int, int, int) { return 256; }
+
+int launch_kv_attend(const AttendArgs &a, cudaStream_t st) {
+    const dim3 grid(a.T, a.hq);
+    if (a.dim == 64 && a.dtype == LORA_BF16) attend_cached_kernel<64, __nv_bfloat16><<<grid, kWarps * 32, 0, st>>>(a);
+    else if (a.dim == 64) attend_cached_kernel<64, __half><<<grid, kWarps * 32, 0, st>>>(a);
+    else if (a.dtype == LORA_BF16) attend_cached_kernel<128, __nv_bfloat16><<<grid, kWarps * 32, 0, st>>>(a);
+    else attend_cached_kernel<128, __half><<<grid, kWarps * 32, 0, st>>>(a);
+    count_launch();
+    return cuda_check(cudaGetLastError());
+}
+
+int launch_prompt(const PromptArgs &a, cudaStream_t st) {
+    const dim3 grid(a.Tq, a.hq);
+    if (a.dim == 64 && a.dtype == LORA_BF16) attend_prompt_kernel<64, __nv_bfloat16><<<grid, kWarps * 32, 0, st>>>(a);
+    else if (a.dim == 64) attend_prompt_kernel<64, __half><<<grid, kWarps * 32, 0, st>>>(a);
+    else if (a.dtype == LORA_BF16) attend_prompt_kernel<128, __nv_bfloat16><<<grid, kWarps * 32, 0, st>>>(a);
+    else attend_prompt_kernel<128, __half><<<grid, kWarps * 32, 0, st>>>(a);
+    count_launch();
+    return cuda_check(cudaGetLastError());
+}
+
+}  // namespace lora

@@ -75,7 +75,10 @@ typedef struct lora_pool_s *lora_pool_t;        /* opaque host handle of one pag
 #define LORA_DEV_ERR_EMPTY_SLOT  2   /* some id names a slot with rank 0 */
 #define LORA_DEV_ERR_TIMEOUT     4   /* a kernel's bounded wait ran out (results of that call are undefined) */
 #define LORA_DEV_ERR_BAD_PAGE    8   /* a used slot's rank exceeds 64 or its page table names a page outside the
-                                        pool; its tokens are skipped */
+                                        pool; its tokens are skipped.  KV-cache calls: a block table entry or a slot
+                                        outside the cache (see each call) */
+#define LORA_DEV_ERR_NO_PAGES   16   /* lora_kv_layout: the free list is too short for a request's new blocks */
+#define LORA_DEV_ERR_BAD_LENGTH 32   /* a request length that is negative or does not fit (see each call) */
 
 /* Fixed geometry. */
 #define LORA_PAGE_ROWS            16   /* rank-rows per page */
@@ -388,6 +391,189 @@ int lora_slot_cache_lookup(lora_slot_cache_t c, int64_t key, int *slot_out);
 int lora_slot_cache_stats(lora_slot_cache_t c, int64_t *hits, int64_t *misses, int64_t *evictions);
 
 /* ------------------------------------------------------------------------ */
+/* Attention side of a step: KV cache in the pool's pages, and attention      */
+/* ------------------------------------------------------------------------ */
+/* Page "Multi-LoRA Serving in Production", section "Unified Paging
+ * Architecture": KV-cache tensors and adapter weights live in pages of one
+ * pool and kernels receive physical page indices; page "LoRA Adapters at Serve
+ * Time with vLLM Multi-LoRA", section "The Inference Mechanism: A Worked
+ * Scenario": KV blocks are allocated per request and each step runs a batch of
+ * requests with their own adapters.  The calls below take a step from the
+ * query, key and value rows that lora_apply_multi leaves (fp32) to attention:
+ * request lengths -> block tables and slots (lora_kv_layout), rotary positions
+ * and the 4-bit cache (lora_rope, lora_kv_append, lora_kv_gather), attention
+ * of new tokens over the cache (lora_kv_attend) and of whole prompts
+ * (lora_prompt_attend).
+ *
+ * Element types of row tensors. */
+#define LORA_BF16 0
+#define LORA_FP16 1
+#define LORA_FP32 2
+
+/* Row tensors [T][heads][head_dim]: element (t, h, d) at data[t * token_stride
+ * + h * head_stride + d].  data is 16-byte aligned and both strides are
+ * multiples of 16 bytes, else LORA_ERR_INVALID_ARG: a column block of a fused
+ * projection output is fine.  Strides count elements and are not negative.
+ * The rows of an output are distinct and overlap no input, except where a
+ * call allows working in place. */
+typedef struct {
+    void *data;
+    int64_t token_stride;
+    int64_t head_stride;
+} lora_rows_t;
+
+/* A KV cache of one layer: num_pages pages of page_bytes bytes each at pages
+ * (16-byte aligned, page_bytes a multiple of 16).  A lora_pool's memory is one:
+ * pages = its dev_buf, page_bytes = LORA_PAGE_ROWS * width * 2, with the pages
+ * that lora_pool_alloc_pages hands out.  Each page holds one block of
+ * block_tokens tokens (a positive multiple of LORA_KV_GRANULE, at most 1024) at
+ * its start, lora_kv_block_bytes(...) <= page_bytes.  head_dim is 64 or 128,
+ * kv_heads 1..256, num_pages * block_tokens at most INT32_MAX.
+ *
+ * Format of a block: [kv head][block_tokens / 16][granule].  A granule holds 16
+ * tokens of one head: K codes [16][head_dim / 2] bytes, K parameters
+ * [16][head_dim / 64] (step, low) pairs of fp16, then V codes and V parameters.
+ * Byte j of a code row holds dimension 2 j in its low and 2 j + 1 in its high
+ * four bits; a code n stands for n * step + low, (step, low) shared by the 64
+ * dimensions of its group. */
+#define LORA_KV_GRANULE 16
+#define LORA_KV_GROUP   64
+typedef struct {
+    void *pages;
+    size_t page_bytes;
+    int num_pages;
+    int kv_heads;
+    int head_dim;
+    int block_tokens;
+} lora_kv_cache_t;
+
+/* Bytes of one block; 0 for sizes that the cache does not take. */
+size_t lora_kv_block_bytes(int kv_heads, int head_dim, int block_tokens);
+
+/* Block tables, slots, positions and adapter ids of a step, from its requests'
+ * lengths, on the device.  Request r holds past_len[r] tokens and brings
+ * new_len[r] more; its blocks are block_table[r][0 .. max_blocks) (page ids),
+ * of which the first ceil(past_len / block_tokens) are filled on entry.  In
+ * request order, every request takes the pages its new tokens need from
+ * free_pages[free_head ..] and has their ids written to its row of block_table
+ * (other entries stay).  free_pages [num_free] and free_head [1] are device
+ * arrays; free_head NULL means 0; free_pages NULL means that block_table
+ * already names every block (the slots of cached tokens can be listed so).
+ * Outputs (device):
+ *   cu_new [R+1]     first row of each request's new tokens; cu_new[R] is the
+ *                    number of rows used
+ *   kv_len [R]       past_len + new_len
+ *   positions [T], slots [T]   position of row t's token and its slot, page *
+ *                    block_tokens + offset; ids [T] (NULL: not wanted) its
+ *                    request's req_ids[r], what lora_plan takes (req_ids NULL: -1)
+ *   free_head_out [1] (NULL: not wanted) first unused place of free_pages
+ * Rows past cu_new[R] get -1 in positions, slots and ids, which every call
+ * below and lora_plan skip.  Inputs and outputs must not overlap (free_head_out
+ * may not be free_head).  R in 1..LORA_KV_MAX_REQUESTS, T >= 0.
+ * A request fails, alone, when a length is negative or past + new exceeds
+ * max_blocks * block_tokens (or its rows exceed T): LORA_DEV_ERR_BAD_LENGTH; or
+ * when the list is too short for it: LORA_DEV_ERR_NO_PAGES.  It takes no
+ * pages, kv_len is 0 and its rows (min(new_len, what is left of T)) get -1
+ * everywhere.  A row whose block has a negative page id gets slot -1 and
+ * LORA_DEV_ERR_BAD_PAGE. */
+#define LORA_KV_MAX_REQUESTS 4096
+int lora_kv_layout(const int32_t *past_len, const int32_t *new_len, const int32_t *req_ids, int R, int T,
+                   int block_tokens, int32_t *block_table, int max_blocks, const int32_t *free_pages, int num_free,
+                   const int32_t *free_head, int32_t *cu_new, int32_t *kv_len, int32_t *positions, int32_t *slots,
+                   int32_t *ids, int32_t *free_head_out, int32_t *err_dev, lora_stream_t stream);
+
+/* Rotary positions.  For each row t with positions[t] >= 0 (others are left
+ * alone, input and output) and each pair i < rot_dim / 2 of every head:
+ *     angle = positions[t] * inv_freq[i]
+ *     (a, b) -> mscale * (a cos - b sin, b cos + a sin)
+ * where (a, b) are dimensions (i, i + rot_dim / 2), or (2 i, 2 i + 1) when
+ * interleaved != 0; dimensions >= rot_dim are copied.  inv_freq [rot_dim / 2]
+ * fp32 on the device carries any scaling for long contexts, mscale its factor
+ * on the rotated part.  The angle, its sine and cosine are formed in 64 bits,
+ * so positions up to INT32_MAX keep their accuracy.
+ *   q [T][q_heads], k [T][k_heads] rows of src_dtype; k_heads = 0: no k.
+ *   head_dim a multiple of 16, at most 256; rot_dim a multiple of 16, at most
+ *   head_dim (0: rows are only converted).
+ *   q_out, k_out rows of dst_dtype, LORA_BF16 or LORA_FP16; src_dtype is
+ *   dst_dtype or LORA_FP32.  With equal types an output may be its input
+ *   (same data and strides). */
+int lora_rope(const lora_rows_t *q, int q_heads, const lora_rows_t *k, int k_heads, int src_dtype, int T, int head_dim,
+              const int32_t *positions, const float *inv_freq, int rot_dim, int interleaved, double mscale,
+              const lora_rows_t *q_out, const lora_rows_t *k_out, int dst_dtype, lora_stream_t stream);
+
+/* lora_rope, then the keys and values of every row with slots[t] >= 0 (and
+ * positions[t] >= 0) written to the cache in 4 bits, in one launch.  What is
+ * cached is the rotated key, and the value, rounded to dst_dtype; per group
+ * of 64 dimensions
+ *     low = fp16(min), step = fp16((max - min) / 15),
+ *     code = clamp(round_even((x - low) / step), 0, 15)      (0 when step = 0)
+ * with every rounding taken from the exact value.  A group that holds a NaN or
+ * an infinity, or spans more than fp16 reaches, reads back as NaN.
+ *   v [T][kv_heads] rows of src_dtype; k_out and v_out (the rounded keys and
+ *   values, for lora_prompt_attend) may be NULL; q may be NULL with q_heads 0.
+ * The slots of a call are distinct.  A slot beyond the cache is skipped and
+ * sets LORA_DEV_ERR_BAD_PAGE. */
+int lora_kv_append(const lora_rows_t *q, int q_heads, const lora_rows_t *k, const lora_rows_t *v, int src_dtype, int T,
+                   const int32_t *positions, const float *inv_freq, int rot_dim, int interleaved, double mscale,
+                   const int32_t *slots, const lora_kv_cache_t *cache, const lora_rows_t *q_out,
+                   const lora_rows_t *k_out, const lora_rows_t *v_out, int dst_dtype, int32_t *err_dev,
+                   lora_stream_t stream);
+
+/* Read the tokens at slots[0 .. T) back: row t of k_out and v_out [T][kv_heads]
+ * (either may be NULL) gets the values the cache holds, n * step + low in fp32
+ * rounded to dst_dtype (any of the three).  Rows with a negative slot are left
+ * alone; a slot beyond the cache leaves its row alone and sets
+ * LORA_DEV_ERR_BAD_PAGE.  With lora_kv_layout(free_pages = NULL) this is how a
+ * cached prefix becomes the dense keys and values of lora_prompt_attend. */
+int lora_kv_gather(const lora_kv_cache_t *cache, const int32_t *slots, int T, const lora_rows_t *k_out,
+                   const lora_rows_t *v_out, int dst_dtype, int32_t *err_dev, lora_stream_t stream);
+
+/* Attention of each request's newest tokens over its cache.  Rows cu_q[r] ..
+ * cu_q[r+1] of q are the last n tokens of request r (already in the cache), so
+ * row cu_q[r] + i, head h, attends to positions j <= kv_len[r] - n + i of kv
+ * head h / (q_heads / kv_heads):
+ *     out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q . k_j)
+ *   q, out [T][q_heads] rows of dtype (LORA_BF16 or LORA_FP16); lse [T][q_heads]
+ *   fp32 (NULL: not wanted) = log sum_j p_j.
+ *   block_table [R][max_blocks], cu_q [R+1], kv_len [R] int32 on the device, as
+ *   lora_kv_layout writes them.  max_q_len: most rows of one request.
+ * Rows outside [cu_q[0], cu_q[R]) are left alone.  A row that attends to nothing
+ * (kv_len 0, or fewer tokens than rows) gets out = 0, lse = -inf.  Keys and
+ * values past the end of a request, its last page's rest included, do not
+ * affect its rows, whatever the cache holds there.  A request with more than
+ * max_q_len rows, rows beyond T, or kv_len beyond max_blocks * block_tokens:
+ * LORA_DEV_ERR_BAD_LENGTH, its rows left alone.  A block whose table entry is
+ * outside the cache is passed over and sets LORA_DEV_ERR_BAD_PAGE.
+ * Softmax statistics and sums are fp32.  ws: lora_kv_attend_workspace_size
+ * bytes, 256-byte aligned, any contents; calls that may overlap on the GPU need
+ * workspaces of their own.  q_heads is a multiple of cache->kv_heads, at most
+ * LORA_KV_MAX_GROUP times it; R in 1..LORA_KV_MAX_REQUESTS. */
+#define LORA_KV_MAX_GROUP 64
+size_t lora_kv_attend_workspace_size(int q_heads, int kv_heads, int head_dim, int max_q_len);
+int lora_kv_attend(const lora_rows_t *q, int T, int q_heads, int dtype, const lora_kv_cache_t *cache,
+                   const int32_t *block_table, int max_blocks, const int32_t *cu_q, const int32_t *kv_len, int R,
+                   int max_q_len, float scale, const lora_rows_t *out, float *lse, void *ws, size_t ws_bytes,
+                   int32_t *err_dev, lora_stream_t stream);
+
+/* Causal attention over packed prompts.  Request r has query rows cu_q[r] ..
+ * cu_q[r+1] (n) and key and value rows cu_k[r] .. cu_k[r+1] (m); query i attends
+ * to keys j <= m - n + i of kv head h / (q_heads / kv_heads), with the formula of
+ * lora_kv_attend.  n = m for whole prompts (cu_k may be cu_q); m > n when a
+ * prefix comes from the cache (lora_kv_gather).
+ *   q, out [Tq][q_heads], k, v [Tk][kv_heads] rows of dtype (LORA_BF16 or
+ *   LORA_FP16), head_dim 64 or 128; lse [Tq][q_heads] fp32 or NULL.  cu_q, cu_k
+ *   [R+1] int32 on the device, not decreasing, within [0, Tq] and [0, Tk]: a
+ *   request that is not sets LORA_DEV_ERR_BAD_LENGTH and its rows are left alone.
+ * Rows outside [cu_q[0], cu_q[R]) are left alone.  A row that attends to nothing
+ * gets out = 0, lse = -inf.  Other requests' rows and rows behind the last one
+ * do not affect a request, whatever they hold (NaN included); within a request,
+ * a value that is not finite may reach rows before it.  Scores and sums are
+ * fp32; the weights p_j are rounded to dtype before they multiply the values. */
+int lora_prompt_attend(const lora_rows_t *q, const lora_rows_t *k, const lora_rows_t *v, int Tq, int Tk, int q_heads,
+                       int kv_heads, int head_dim, int dtype, const int32_t *cu_q, const int32_t *cu_k, int R,
+                       float scale, const lora_rows_t *out, float *lse, int32_t *err_dev, lora_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Options and diagnostics (process-wide)                                   */
 /* ------------------------------------------------------------------------ */
 
@@ -419,7 +605,8 @@ int lora_get_option(int key);
 const char *lora_last_cuda_error(void);
 
 /* Number of kernels launched by the last lora_apply / lora_shrink /
- * lora_expand_add / lora_plan call on the calling host thread. */
+ * lora_expand_add / lora_plan / lora_kv_* / lora_rope / lora_prompt_attend
+ * call on the calling host thread. */
 int lora_last_launch_count(void);
 
 #ifdef __cplusplus
