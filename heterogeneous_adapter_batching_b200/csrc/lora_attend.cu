@@ -72,7 +72,7 @@ __device__ __forceinline__ void attend_row(const Kv &kv, int n, const H *q, H *o
 #pragma unroll
         for (int i = 0; i < E; ++i) s = fmaf(qv[i], k[i], s);
         for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-        const float mn = fmaxf(m, s), f = m == -INFINITY ? 0.f : __expf(m - mn), p = mn == -INFINITY ? 0.f : __expf(s - mn);
+        const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn, f = __expf(m - ref), p = __expf(s - ref);
         l = l * f + p;
 #pragma unroll
         for (int i = 0; i < E; ++i) acc[i] = acc[i] * f + (p > 0.f || p != p ? p * v[i] : 0.f);
@@ -87,58 +87,53 @@ __device__ __forceinline__ void attend_row(const Kv &kv, int n, const H *q, H *o
     __syncthreads();
     float mm = -INFINITY, ll = 0.f;
     for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w]);
-    for (int w = 0; w < kWarps; ++w) ll += sm_m[w] == -INFINITY ? 0.f : sm_l[w] * __expf(sm_m[w] - mm);
+    const float ref = mm == -INFINITY ? 0.f : mm;   // scores may all be NaN
+    for (int w = 0; w < kWarps; ++w) ll += sm_l[w] * __expf(sm_m[w] - ref);
     for (int d = threadIdx.x; d < DIM; d += kWarps * 32) {
         float s = 0.f;
-        for (int w = 0; w < kWarps; ++w) s += sm_m[w] == -INFINITY ? 0.f : sm_o[w][d] * __expf(sm_m[w] - mm);
-        o[d] = (H)(mm == -INFINITY ? 0.f : s / ll);
+        for (int w = 0; w < kWarps; ++w) s += sm_o[w][d] * __expf(sm_m[w] - ref);
+        o[d] = (H)(ll == 0.f ? 0.f : s / ll);
     }
-    if (lse && threadIdx.x == 0) *lse = mm == -INFINITY ? -INFINITY : mm + logf(ll);
-}
-
-// First request whose rows end after t (R: none).
-__device__ __forceinline__ int request_of(const int32_t *cu, int R, int t) {
-    int lo = 0, hi = R;
-    while (lo < hi) {
-        const int m = (lo + hi) >> 1;
-        if (cu[m + 1] > t) hi = m;
-        else lo = m + 1;
-    }
-    return lo;
+    if (lse && threadIdx.x == 0) *lse = ref + logf(ll);
 }
 
 template <int DIM, class H>
 __global__ void __launch_bounds__(kWarps * 32) attend_cached_kernel(AttendArgs a) {
     const int t = blockIdx.x, hq = blockIdx.y;
-    const int r = request_of(a.cu_q, a.R, t);
-    if (r >= a.R || t < a.cu_q[r]) return;
-    const int q0 = a.cu_q[r], n = a.cu_q[r + 1] - q0, len = a.kv_len[r];
-    if (n > a.max_q || len < 0 || (long long)len > (long long)a.max_blocks * a.c.block) {
-        if (a.err && threadIdx.x == 0) atomicOr(a.err, LORA_DEV_ERR_BAD_LENGTH);
-        return;
+    for (int r = 0; r < a.R; ++r) {
+        const int q0 = a.cu_q[r], q1 = a.cu_q[r + 1], n = q1 - q0, len = a.kv_len[r];
+        if (q0 == q1) continue;
+        if (q0 < 0 || q1 < q0 || q1 > a.T || n > a.max_q || len < 0 || (long long)len > (long long)a.max_blocks * a.c.block) {
+            if (a.err && threadIdx.x == 0 && t == 0 && hq == 0) atomicOr(a.err, LORA_DEV_ERR_BAD_LENGTH);
+            continue;
+        }
+        if (t < q0 || t >= q1) continue;
+        __syncthreads();
+        const CachedKv<DIM> kv{a.c, a.table + (size_t)r * a.max_blocks, hq / (a.hq / a.c.heads), a.err};
+        attend_row<DIM, H>(kv, len - n + (t - q0) + 1, reinterpret_cast<const H *>(a.q.p) + t * a.q.ts + hq * a.q.hs,
+                           reinterpret_cast<H *>(a.o.p) + t * a.o.ts + hq * a.o.hs,
+                           a.lse ? a.lse + (size_t)t * a.hq + hq : nullptr, a.scale);
     }
-    const CachedKv<DIM> kv{a.c, a.table + (size_t)r * a.max_blocks, hq / (a.hq / a.c.heads), a.err};
-    attend_row<DIM, H>(kv, len - n + (t - q0) + 1, reinterpret_cast<const H *>(a.q.p) + t * a.q.ts + hq * a.q.hs,
-                       reinterpret_cast<H *>(a.o.p) + t * a.o.ts + hq * a.o.hs,
-                       a.lse ? a.lse + (size_t)t * a.hq + hq : nullptr, a.scale);
 }
 
 template <int DIM, class H>
 __global__ void __launch_bounds__(kWarps * 32) attend_prompt_kernel(PromptArgs a) {
     const int t = blockIdx.x, hq = blockIdx.y, h = hq / (a.hq / a.hkv);
-    const int r = request_of(a.cu_q, a.R, t);
-    if (r >= a.R || t < a.cu_q[r]) return;
-    const int q0 = a.cu_q[r], q1 = a.cu_q[r + 1], k0 = a.cu_k[r], k1 = a.cu_k[r + 1];
-    if (q0 < 0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk) {
-        if (a.err && threadIdx.x == 0) atomicOr(a.err, LORA_DEV_ERR_BAD_LENGTH);
-        return;
+    for (int r = 0; r < a.R; ++r) {
+        const int q0 = a.cu_q[r], q1 = a.cu_q[r + 1], k0 = a.cu_k[r], k1 = a.cu_k[r + 1];
+        if (q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk) {
+            if (a.err && threadIdx.x == 0 && t == 0 && hq == 0) atomicOr(a.err, LORA_DEV_ERR_BAD_LENGTH);
+            continue;
+        }
+        if (t < q0 || t >= q1) continue;
+        __syncthreads();
+        const DenseKv<DIM, H> kv{reinterpret_cast<const H *>(a.k.p) + k0 * a.k.ts + h * a.k.hs,
+                                 reinterpret_cast<const H *>(a.v.p) + k0 * a.v.ts + h * a.v.hs, a.k.ts, a.v.ts};
+        attend_row<DIM, H>(kv, (k1 - k0) - (q1 - q0) + (t - q0) + 1,
+                           reinterpret_cast<const H *>(a.q.p) + t * a.q.ts + hq * a.q.hs,
+                           reinterpret_cast<H *>(a.o.p) + t * a.o.ts + hq * a.o.hs,
+                           a.lse ? a.lse + (size_t)t * a.hq + hq : nullptr, a.scale);
     }
-    const DenseKv<DIM, H> kv{reinterpret_cast<const H *>(a.k.p) + k0 * a.k.ts + h * a.k.hs,
-                             reinterpret_cast<const H *>(a.v.p) + k0 * a.v.ts + h * a.v.hs, a.k.ts, a.v.ts};
-    attend_row<DIM, H>(kv, (k1 - k0) - (q1 - q0) + (t - q0) + 1,
-                       reinterpret_cast<const H *>(a.q.p) + t * a.q.ts + hq * a.q.hs,
-                       reinterpret_cast<H *>(a.o.p) + t * a.o.ts + hq * a.o.hs,
-                       a.lse ? a.lse + (size_t)t * a.hq + hq : nullptr, a.scale);
 }
 
 }  // namespace

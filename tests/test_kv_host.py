@@ -1,0 +1,173 @@
+"""CPU checks of the KV-cache and attention calls: sizes, argument refusals before
+any CUDA call, and the binding's own checks."""
+import ctypes
+
+import pytest
+import torch
+
+from tests import _kv as K
+
+FAKE = 0x7F0000000000      # aligned, never dereferenced
+
+
+@pytest.fixture(scope="module")
+def H():
+    from heterogeneous_adapter_batching_b200 import build
+    build.build()
+    import heterogeneous_adapter_batching_b200 as H
+    H.load_library()
+    return H
+
+
+def p(off=0):
+    return ctypes.c_void_p(FAKE + off)
+
+
+def rows(H, off=0, ts=1024, hs=128):
+    return ctypes.byref(H.LoraRows(FAKE + off, ts, hs))
+
+
+def cache(H, **kw):
+    a = dict(pages=FAKE, page_bytes=1 << 20, num_pages=64, kv_heads=8, head_dim=128, block_tokens=64)
+    a.update(kw)
+    return ctypes.byref(H.LoraKvCache(**a))
+
+
+def test_block_bytes(H):
+    for heads in (1, 2, 8, 256):
+        for dim in (64, 128):
+            for block in (16, 96, 1024):
+                n = H.lora_kv_block_bytes(heads, dim, block)
+                assert n == K.block_bytes(heads, dim, block) and n % 128 == 0
+    for bad in ((0, 128, 16), (257, 128, 16), (8, 96, 16), (8, 256, 16), (8, 128, 0), (8, 128, 17), (8, 128, 1040), (-1, 128, 16)):
+        assert H.lora_kv_block_bytes(*bad) == 0
+
+
+def test_layout_refusals(H):
+    lib = H.load_library()
+
+    def call(past=p(), new=p(), R=4, T=8, block=16, table=p(), width=4, free=p(), nfree=10, head=p(64), cu=p(), kv=p(), pos=p(),
+             slots=p(), out=p(128)):
+        return lib.lora_kv_layout(past, new, None, R, T, block, table, width, free, nfree, head, cu, kv, pos, slots, None, out, None, None)
+
+    assert call(past=None) == -1 and call(new=None) == -1 and call(table=None) == -1 and call(cu=None) == -1 and call(kv=None) == -1
+    assert call(pos=None) == -1 and call(slots=None) == -1
+    assert call(R=0) == -1 and call(T=-1) == -1 and call(width=0) == -1 and call(nfree=-1) == -1
+    assert call(block=0) == -1 and call(block=24) == -1 and call(block=1040) == -1
+    assert call(head=p(64), out=p(64)) == -1                    # the list's head is not updated in place
+    assert call(R=4097) == -8 and call(width=2 ** 31 // 16) == -8
+    assert lib.lora_last_launch_count() == 0
+
+
+def test_rope_refusals(H):
+    lib = H.load_library()
+
+    def call(q=None, hq=8, k=None, hk=2, src=0, T=4, dim=128, pos=p(), freq=p(), rot=128, qo=None, ko=None, dst=0):
+        q, k, qo, ko = (rows(H) if x is None else x for x in (q, k, qo, ko))
+        return lib.lora_rope(q, hq, k, hk, src, T, dim, pos, freq, rot, 0, 1.0, qo, ko, dst, None)
+
+    assert call(T=0) == 0 and call(hq=0, hk=0) == 0             # nothing to do
+    assert call(T=-1) == -1 and call(pos=None) == -1 and call(freq=None) == -1
+    assert call(dim=120) == -1 and call(dim=272) == -1 and call(dim=0) == -1
+    assert call(rot=8) == -1 and call(rot=144) == -1 and call(rot=-16) == -1
+    assert call(src=3) == -1 and call(dst=2) == -1 and call(src=0, dst=1) == -1 and call(src=2, dst=2) == -1
+    assert call(q=rows(H, 8)) == -1                             # 16-byte alignment
+    assert call(k=rows(H, ts=1028)) == -1 and call(qo=rows(H, hs=132)) == -1 and call(ko=rows(H, ts=-1024)) == -1
+    assert call(src=2, q=rows(H, ts=1020), k=rows(H, ts=1020), T=0) == 0   # four fp32 values are 16 bytes
+    assert call(hq=-1) == -1 and call(hk=-1) == -1
+    assert lib.lora_last_launch_count() == 0
+
+
+def test_append_and_gather_refusals(H):
+    lib = H.load_library()
+
+    def app(kv=None, T=4, hq=8, q=None, k=None, v=None, slots=p(), ko=None, src=0, dst=0):
+        kv = cache(H) if kv is None else kv
+        q, k, v = (rows(H) if x is None else x for x in (q, k, v))
+        return lib.lora_kv_append(q, hq, k, v, src, T, p(), p(), 128, 0, 1.0, slots, kv, rows(H), ko, None, dst, None, None)
+
+    def gat(kv=None, slots=p(), T=4, ko=None, dst=0):
+        return lib.lora_kv_gather(cache(H) if kv is None else kv, slots, T, rows(H) if ko is None else ko, None, dst, None, None)
+
+    assert app(T=0) == 0 and gat(T=0) == 0
+    assert lib.lora_kv_gather(cache(H), p(), 4, None, None, 0, None, None) == 0
+    for bad in (dict(pages=None), dict(pages=FAKE + 8), dict(page_bytes=(1 << 20) + 8), dict(num_pages=0), dict(kv_heads=0),
+                dict(head_dim=96), dict(block_tokens=40), dict(page_bytes=K.block_bytes(8, 128, 64) - 16)):
+        assert app(kv=cache(H, **bad)) == -1, bad
+        assert gat(kv=cache(H, **bad)) == -1, bad
+    assert app(kv=cache(H, num_pages=2 ** 31 // 64)) == -8 and gat(kv=cache(H, num_pages=2 ** 31 // 64)) == -8
+    assert app(slots=None) == -1 and gat(slots=None) == -1 and app(T=-1) == -1 and gat(T=-1) == -1
+    assert app(v=rows(H, 4)) == -1 and app(ko=rows(H, ts=4)) == -1 and gat(ko=rows(H, hs=12)) == -1
+    assert app(src=1, dst=0) == -1 and gat(dst=3) == -1
+    assert lib.lora_last_launch_count() == 0
+
+
+def test_attend_refusals(H):
+    lib = H.load_library()
+    n = H.lora_kv_attend_workspace_size(32, 8, 128, 1)
+    assert n > 0 and n % 256 == 0
+    assert H.lora_kv_attend_workspace_size(30, 8, 128, 1) == 0 and H.lora_kv_attend_workspace_size(32, 8, 96, 1) == 0
+    assert H.lora_kv_attend_workspace_size(32, 8, 128, 0) == 0 and H.lora_kv_attend_workspace_size(0, 8, 128, 1) == 0
+
+    def call(q=None, T=4, hq=32, dtype=0, kv=None, table=p(), width=4, cu=p(), lens=p(), R=4, mq=1, out=None, ws=p(), nb=n):
+        q, out = (rows(H) if x is None else x for x in (q, out))
+        return lib.lora_kv_attend(q, T, hq, dtype, cache(H) if kv is None else kv, table, width, cu, lens, R, mq, 1.0, out, None, ws, nb,
+                                  None, None)
+
+    assert call(T=0) == 0
+    assert call(hq=30) == -1 and call(hq=0) == -1 and call(hq=8 * 65) == -1
+    assert call(dtype=2) == -1 and call(T=-1) == -1 and call(R=0) == -1 and call(mq=0) == -1 and call(width=0) == -1
+    assert call(table=None) == -1 and call(cu=None) == -1 and call(lens=None) == -1
+    assert call(q=rows(H, 2)) == -1 and call(out=rows(H, ts=1025)) == -1
+    assert call(ws=None) == -7 and call(ws=p(16)) == -7 and call(nb=n - 1) == -7
+    assert call(R=4097) == -8 and call(width=2 ** 31 // 64) == -8
+    assert call(kv=cache(H, head_dim=80)) == -1
+    assert lib.lora_last_launch_count() == 0
+
+
+def test_prompt_refusals(H):
+    lib = H.load_library()
+
+    def call(q=None, k=None, v=None, Tq=4, Tk=4, hq=32, hk=8, dim=128, dtype=0, cq=p(), ck=p(), R=1, out=None):
+        q, k, v, out = (rows(H) if x is None else x for x in (q, k, v, out))
+        return lib.lora_prompt_attend(q, k, v, Tq, Tk, hq, hk, dim, dtype, cq, ck, R, 1.0, out, None, None, None)
+
+    assert call(Tq=0) == 0
+    assert call(Tq=-1) == -1 and call(Tk=-1) == -1 and call(R=0) == -1 and call(cq=None) == -1 and call(ck=None) == -1
+    assert call(hq=31) == -1 and call(hk=0) == -1 and call(dim=96) == -1 and call(dim=256) == -1 and call(dtype=2) == -1
+    assert call(k=rows(H, 8)) == -1 and call(v=rows(H, ts=1026)) == -1 and call(out=rows(H, hs=-128)) == -1
+    assert call(R=4097) == -8
+    assert lib.lora_last_launch_count() == 0
+
+
+def test_binding_refuses_what_it_cannot_pass(H):
+    t = torch.zeros
+    q, i = t((4, 8, 128), dtype=torch.bfloat16), t(4, dtype=torch.int32)
+    f = t(64)
+    for call in (lambda: H.lora_rope(q, None, i, f, q), lambda: H.lora_prompt_attend(q, q, q, i, i, 1.0, q),
+                 lambda: H.lora_kv_gather(q[0], 16, i, q), lambda: H.lora_kv_append(None, q, q, i, f, i, q[0], 16, None),
+                 lambda: H.lora_kv_attend(q, q[0], 16, 8, t((4, 2), dtype=torch.int32), i, i, 1, 1.0, q, f),
+                 lambda: H.lora_kv_layout(i, i, None, 16, t((4, 2), dtype=torch.int32), None, None, i, i, i, i)):
+        with pytest.raises(H.LoraError):   # tensors of the host
+            call()
+
+
+def test_reference_quantiser_and_page_format():
+    """The reference itself: closed forms, and a page written by hand."""
+    import numpy as np
+    x = torch.zeros((1, 1, 128), dtype=torch.bfloat16)
+    x[0, 0, :64] = torch.arange(64) % 16                # low 0, step 1: codes are the values
+    x[0, 0, 64:] = -2.5                                 # a constant group: step 0, low the value
+    n, s, lo = K.quantise(x)
+    assert n[0, 0, :64].tolist() == [i % 16 for i in range(64)] and n[0, 0, 64:].max() == 0
+    assert s[0, 0].tolist() == [1.0, 0.0] and lo[0, 0].tolist() == [0.0, -2.5]
+    assert K.value(n, s, lo)[0, 0].tolist() == x[0, 0].float().tolist()
+    b = np.zeros((2, K.block_bytes(2, 128, 32)), dtype=np.uint8)
+    c = K.Cache(b, 2, 128, 32)
+    c.write(32 + 17, 1, 1, n[0, 0], s[0, 0], lo[0, 0])  # page 1, second granule, row 1, head 1, the V half
+    base = (1 * 2 + 1) * 2304 + 1152
+    assert b[1, base + 64:base + 128].tolist() == [(2 * j % 16) | ((2 * j + 1) % 16) << 4 for j in range(32)] + [0] * 32
+    assert b[1, base + 1024 + 8:base + 1024 + 16].view(np.float16).tolist() == [1.0, 0.0, 0.0, -2.5]
+    assert b[0].max() == 0
+    got = c.read(49, 1, 1)
+    assert all((a == w).all() for a, w in zip(got, (n[0, 0], s[0, 0], lo[0, 0])))
