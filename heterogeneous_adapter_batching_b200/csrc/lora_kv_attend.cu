@@ -1,0 +1,707 @@
+// Attention of each request's newest tokens over the paged 4-bit cache.
+//
+// out = sum_j p_j v_j / sum_j p_j, p_j = exp(scale q . k_j), one pass over the
+// cache with a running reference for the exponent.  Every cached byte is read
+// once per 8 (16) query columns, so with few new tokens the cache's bytes bound
+// it; per byte there are two values to unpack, so the unpacking must stay near
+// one instruction per value to keep up with memory.
+//
+// Columns: the new rows of a request times the q heads of one kv head, row
+// major; a tile of NC = 8 NT of them shares one reading of the cache.  Per
+// granule (16 tokens) a warp forms S^T = K Q^T and O^T += V^T P^T with
+// m16n8k16 products whose A operand is the unpacked cache (tokens x dims, then
+// dims x tokens) and whose N = 8 dimension is the columns, so that even 4 heads
+// per kv head waste only half a column tile.  The order of dimensions inside an
+// operand is free as long as both sides use it, and so is the order of tokens:
+// a thread reads whole words of codes from shared memory and a mask-and-or
+// turns bit fields into numbers.
+//   K, bf16 queries: field | 0x4300 is the bf16 number 128 + n; the offset is
+//   taken out of the finished product with the row sums of q (scores keep
+//   about 2^-19 of sum |q| |k|, far below what bf16 queries carry).
+//   K, fp16 queries, and V: field | 0x6400 is the fp16 number 1024 + n (or
+//   1024 + 16 n for the odd fields); one fused multiply-add makes it n - 8.
+// So the products take exact integers; steps and lows enter in fp32: a score is
+// step * (q . n) + low * sum q per group of 64 dimensions, the weight of a value
+// is p * step per group, and sum p * (low + 8 step) is kept apart.  p * step is
+// rounded to fp16 (2^-11 relative: an eighth of a bf16 step) after scaling by
+// 32 / sref, sref the largest step so far rounded up to a power of two, so that
+// neither small steps nor small weights leave fp16's range.  Everything else is
+// fp32.
+//
+// The exponent's reference m is only moved when a score exceeds it by 10 (in
+// powers of two): weights then reach at most 2^10 * 32 in fp16, and the usual
+// granule needs no reduction over the warp for its maximum.
+//
+// Work split: a unit is 4 granules (64 tokens) of one (request, kv head, column
+// tile); the units of the batch are numbered and every CTA takes an equal
+// contiguous range, whatever the lengths.  Inside a CTA, 4 warps take granules
+// in turn, each with its own ring of cp.async stages that runs ahead across
+// (request, head) borders, and are joined in shared memory at the end of a
+// piece.  A piece that is not a whole (request, head, tile) leaves its sums in
+// the workspace (at most two per CTA: its first and its last), and a second
+// launch joins those in order.
+#include <type_traits>
+
+#include "lora_internal.cuh"
+#include "lora_kv.cuh"
+#include "lora_ptx.cuh"
+
+namespace lora {
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kRound = kWarps * LORA_KV_GRANULE;   // tokens of a unit
+constexpr int kMaxCtas = 592;                      // 4 CTAs on each of 148 SMs
+constexpr int kStages = 4;
+constexpr float kJump = 10.f;                      // log2 by which a score may exceed the reference
+constexpr int kShift = 5;                          // weights are scaled by 2^kShift in fp16
+constexpr int kJoinGroups = 4;                     // thread groups of the joining kernel
+
+// What a CTA leaves for the joining kernel about the segment that begins in it and ends in CTA `last`.
+struct Split {
+    int r, h, ct, last;   // last = 0: none
+};
+
+template <int DIM, int NT>
+struct Smem {
+    alignas(128) unsigned char ring[kWarps][kStages][kv_granule_bytes(DIM)];
+    float o[kWarps][8 * NT][DIM + 4];
+    float m[kWarps][8 * NT], l[kWarps][8 * NT];
+    long long scan[kWarps];
+    long long base;
+    int first;
+};
+
+constexpr size_t partial_floats(int dim, int nc) { return (size_t)nc * (dim + 2); }   // O, then m, then l
+
+struct Req {
+    int q0, nq, len, rounds, tiles;
+};
+
+template <int NC>
+__device__ __forceinline__ Req load_req(const AttendArgs &a, int r, int G, bool &bad) {
+    Req q;
+    q.q0 = a.cu_q[r];
+    const int q1 = a.cu_q[r + 1];
+    q.len = a.kv_len[r];
+    q.nq = q1 - q.q0;
+    bad = q1 != q.q0 && (q.q0 < 0 || q1 < q.q0 || q1 > a.T || q.nq > a.max_q || q.len < 0 ||
+                         (long long)q.len > (long long)a.max_blocks * a.c.block);
+    if (bad || q1 == q.q0) q.nq = 0;
+    q.tiles = (q.nq * G + NC - 1) / NC;
+    q.rounds = q.len <= 0 ? 1 : (q.len + kRound - 1) / kRound;
+    return q;
+}
+
+// A walk over this CTA's pieces in order.
+template <int NC>
+struct Walk {
+    Req q;
+    int r, h, ct, round, n;   // current piece: rounds [round, round + n) of (r, h, ct)
+    long long left;           // units after this piece
+    __device__ __forceinline__ void start(const AttendArgs &a, int G, int r0, long long off, long long units) {
+        r = r0;
+        bool bad;
+        q = load_req<NC>(a, r, G, bad);
+        const long long seg = off / q.rounds;
+        round = (int)(off - seg * q.rounds);
+        h = (int)(seg / q.tiles);
+        ct = (int)(seg - (long long)h * q.tiles);
+        n = (int)min((long long)(q.rounds - round), units);
+        left = units - n;
+    }
+    __device__ __forceinline__ bool next(const AttendArgs &a, int G) {
+        if (left == 0) return false;
+        round = 0;
+        if (++ct == q.tiles) {
+            ct = 0;
+            if (++h == a.c.heads) {
+                h = 0;
+                bool bad;
+                do q = load_req<NC>(a, ++r, G, bad);
+                while (q.nq == 0);
+            }
+        }
+        n = (int)min((long long)q.rounds, left);
+        left -= n;
+        return true;
+    }
+    // granules of the piece: [g0, g1)
+    __device__ __forceinline__ int g0() const { return round * kWarps; }
+    __device__ __forceinline__ int g1() const {
+        const int all = q.len <= 0 ? 0 : (q.len + LORA_KV_GRANULE - 1) / LORA_KV_GRANULE;
+        return min(all, (round + n) * kWarps);
+    }
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t mov_trans(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+__device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t y;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
+    return y;
+}
+// d += a b on fp16 (BF = false) or bf16 operands, fp32 accumulators.
+template <bool BF>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    if (BF)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};" : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};" : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Four fp16 pairs n - 8 from the fields of w: pair j holds fields j and j + 4.
+__device__ __forceinline__ void unpack_h(uint32_t w, uint32_t (&x)[4]) {
+    const uint32_t one = 0x3c003c00u, sub = 0xe408e408u /* -1032 */, sixteenth = 0x2c002c00u, sub72 = 0xd480d480u /* -72 */;
+    const uint32_t v = w >> 8;
+    x[0] = fma_h2((w & 0x000f000fu) | 0x64006400u, one, sub);
+    x[1] = fma_h2((w & 0x00f000f0u) | 0x64006400u, sixteenth, sub72);
+    x[2] = fma_h2((v & 0x000f000fu) | 0x64006400u, one, sub);
+    x[3] = fma_h2((v & 0x00f000f0u) | 0x64006400u, sixteenth, sub72);
+}
+// Four bf16 pairs 128 + n.
+__device__ __forceinline__ void unpack_b(uint32_t w, uint32_t (&x)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u;
+}
+
+template <int DIM, int NT, bool BF>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(AttendArgs a, Split *split, float *part) {
+    using H = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+    constexpr int NC = 8 * NT, NG = DIM / LORA_KV_GROUP, GB = kv_granule_bytes(DIM), HB = kv_half_bytes(DIM), CB = kv_code_bytes(DIM);
+    extern __shared__ unsigned char smem_raw[];
+    Smem<DIM, NT> &sm = *reinterpret_cast<Smem<DIM, NT> *>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+    const int G = a.hq / a.c.heads;
+
+    // Units of the batch and this CTA's range of them.
+    const int per = (a.R + kThreads - 1) / kThreads, ra = min(a.R, tid * per), rb = min(a.R, ra + per);
+    long long mine = 0;
+    bool any_bad = false;
+    for (int r = ra; r < rb; ++r) {
+        bool bad;
+        const Req q = load_req<NC>(a, r, G, bad);
+        mine += (long long)q.tiles * q.rounds * a.c.heads;
+        any_bad |= bad;
+    }
+    if (any_bad && blockIdx.x == 0 && a.err) atomicOr(a.err, LORA_DEV_ERR_BAD_LENGTH);
+    long long run = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(~0u, run, d);
+        if (lane >= d) run += x;
+    }
+    if (lane == 31) sm.scan[warp] = run;
+    __syncthreads();
+    long long total = 0;
+    run -= mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) run += sm.scan[w];
+        total += sm.scan[w];
+    }
+    const long long ctas = min((long long)gridDim.x, total);
+    const long long u0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
+    const long long u1 = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : total;
+    if (u0 >= u1) {
+        if (tid == 0) split[blockIdx.x].last = 0;
+        return;
+    }
+    if (run <= u0 && u0 < run + mine) {
+        long long base = run;
+        int r = ra;
+        for (;; ++r) {
+            bool bad;
+            const Req q = load_req<NC>(a, r, G, bad);
+            const long long n = (long long)q.tiles * q.rounds * a.c.heads;
+            if (u0 < base + n) break;
+            base += n;
+        }
+        sm.first = r;
+        sm.base = base;
+    }
+    __syncthreads();
+    Walk<NC> load, comp;
+    comp.start(a, G, sm.first, u0 - sm.base, u1 - u0);
+    load = comp;
+
+    // The warp's granules, in order, into its ring.
+    const uint32_t ring = ptx::smem_u32(sm.ring[warp]);
+    int lg = load.g0() + warp, lend = load.g1(), ids = 0, ids_from = lg;
+    bool more = true;
+    uint32_t valid = 0;   // bit s: stage s holds a granule
+    int in_slot = 0;
+    const auto fetch_ids = [&]() {   // table entries of the warp's next 32 granules of the piece
+        ids_from = lg;
+        const int gi = lg + kWarps * lane;
+        ids = gi < lend ? a.table[(size_t)load.r * a.max_blocks + gi / a.c.granules] : 0;
+    };
+    const auto advance = [&]() {
+        while (more && lg >= lend) {
+            more = load.next(a, G);
+            if (more) {
+                lg = load.g0() + warp;
+                lend = load.g1();
+                if (lg < lend) fetch_ids();
+            }
+        }
+    };
+    const auto issue = [&]() {
+        valid &= ~(1u << in_slot);
+        if (more) {
+            if (lg - ids_from >= 32 * kWarps) fetch_ids();
+            const int page = __shfl_sync(~0u, ids, (lg - ids_from) / kWarps);
+            if (page >= 0 && page < a.c.num_pages) {
+                const unsigned char *src = a.c.pages + page * a.c.page_bytes +
+                                           (long long)(load.h * a.c.granules + lg % a.c.granules) * GB;
+                const uint32_t dst = ring + in_slot * GB;
+#pragma unroll
+                for (int i = 0; i < GB / 512; ++i) cp16(dst + (lane + 32 * i) * 16, src + (lane + 32 * i) * 16);
+                if (lane < GB % 512 / 16) cp16(dst + (lane + GB / 512 * 32) * 16, src + (lane + GB / 512 * 32) * 16);
+                valid |= 1u << in_slot;
+            } else if (lane == 0 && a.err) {
+                atomicOr(a.err, LORA_DEV_ERR_BAD_PAGE);
+            }
+            lg += kWarps;
+            advance();
+        }
+        cp_commit();
+        in_slot = in_slot + 1 == kStages ? 0 : in_slot + 1;
+    };
+    if (lg < lend) fetch_ids();
+    advance();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue();
+
+    const float c = a.scale * 1.4426950408889634f;
+    const int tok = g ^ ((g >> 1) & 1);   // token (of 8) in the operands' row g: both tokens of a pair on different banks
+    int out_slot = 0;
+    bool first_piece = true;
+    if (tid == 0) split[blockIdx.x].last = 0;
+    for (;;) {
+        // Queries of this piece: fragments, and per group their sums.
+        uint32_t qf[NT][NG][4][2];
+        float qs[NT][NG][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int gc = comp.ct * NC + nt * 8 + g;
+            const bool ok = gc < comp.q.nq * G;
+            const int qi = gc / G, head = comp.h * G + gc - qi * G;
+            const H *row = reinterpret_cast<const H *>(a.q.p) + (long long)(comp.q.q0 + qi) * a.q.ts + (long long)head * a.q.hs;
+#pragma unroll
+            for (int ng = 0; ng < NG; ++ng) {
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (ok) u = *reinterpret_cast<const uint4 *>(row + 64 * ng + 16 * t4 + 8 * i);
+                    const H *e = reinterpret_cast<const H *>(&u);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum += (float)e[j];
+                    // pairs (j, j + 4) of the eight dimensions, as the codes unpack
+                    qf[nt][ng][2 * i][0] = __byte_perm(u.x, u.z, 0x5410);
+                    qf[nt][ng][2 * i][1] = __byte_perm(u.x, u.z, 0x7632);
+                    qf[nt][ng][2 * i + 1][0] = __byte_perm(u.y, u.w, 0x5410);
+                    qf[nt][ng][2 * i + 1][1] = __byte_perm(u.y, u.w, 0x7632);
+                }
+                sum += __shfl_xor_sync(~0u, sum, 1);
+                sum += __shfl_xor_sync(~0u, sum, 2);
+                qs[nt][ng][0] = __shfl_sync(~0u, sum, 8 * t4);
+                qs[nt][ng][1] = __shfl_sync(~0u, sum, 8 * t4 + 4);
+            }
+        }
+        // Last key each of the thread's columns sees, and the least of the tile.
+        int lim[NT][2];
+        const int back = comp.q.len - comp.q.nq, least = back + comp.ct * NC / G;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) lim[nt][e] = back + min(comp.q.nq - 1, (comp.ct * NC + nt * 8 + 2 * t4 + e) / G);
+
+        float o[NT][NG][4][4] = {}, om[NT][NG][2] = {}, l[NT][2] = {}, m[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY;
+        float sref = 0.f, rs = 0.f;   // largest step so far as a power of two; 2^kShift over it
+
+        const int gend = comp.g1();
+        for (int gi = comp.g0() + warp; gi < gend; gi += kWarps) {
+            cp_wait<kStages - 2>();
+            __syncwarp();
+            issue();
+            const bool here = (valid >> out_slot) & 1;
+            const unsigned char *st = sm.ring[warp][out_slot];
+            out_slot = out_slot + 1 == kStages ? 0 : out_slot + 1;
+            if (!here) continue;
+
+            // S^T = K Q^T: rows g and g + 8 of the operand are tokens tok and tok + 8.
+            float acc[NT][NG][4] = {};
+#pragma unroll
+            for (int ng = 0; ng < NG; ++ng) {
+                const uint2 w0 = *reinterpret_cast<const uint2 *>(st + tok * (DIM / 2) + 32 * ng + 8 * t4);
+                const uint2 w1 = *reinterpret_cast<const uint2 *>(st + (tok + 8) * (DIM / 2) + 32 * ng + 8 * t4);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t x[4], y[4];
+                    if (BF) {
+                        unpack_b(i ? w0.y : w0.x, x);
+                        unpack_b(i ? w1.y : w1.x, y);
+                    } else {
+                        unpack_h(i ? w0.y : w0.x, x);
+                        unpack_h(i ? w1.y : w1.x, y);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        // fields (0, 4) and (1, 5) against dimensions 0, 4 and 1, 5; then (2, 6) and (3, 7)
+                        mma<BF>(acc[nt][ng], x[0], y[0], x[1], y[1], qf[nt][ng][2 * i][0], qf[nt][ng][2 * i][1]);
+                        mma<BF>(acc[nt][ng], x[2], y[2], x[3], y[3], qf[nt][ng][2 * i + 1][0], qf[nt][ng][2 * i + 1][1]);
+                    }
+                }
+            }
+            // Scores in powers of two.
+            float s[NT][4] = {};
+#pragma unroll
+            for (int ng = 0; ng < NG; ++ng) {
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(st + CB + (tok + 8 * w) * 4 * NG + 4 * ng));
+                    const float sc = p.x * c, lc = fmaf(BF ? -128.f : 8.f, sc, p.y * c);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            s[nt][2 * w + e] = fmaf(sc, acc[nt][ng][2 * w + e], fmaf(lc, qs[nt][ng][e], s[nt][2 * w + e]));
+                }
+            }
+            const int j0 = gi * LORA_KV_GRANULE;
+            const bool edge = j0 + LORA_KV_GRANULE - 1 > least;
+            if (edge) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (j0 + tok + 8 * (e >> 1) > lim[nt][e & 1]) s[nt][e] = -INFINITY;
+            }
+            // Steps and lows of the values.
+            float vs[NG][2], vl[NG][2];
+            bool up = false;
+#pragma unroll
+            for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(st + HB + CB + (tok + 8 * w) * 4 * NG + 4 * ng));
+                    const bool gone = edge && j0 + tok + 8 * w >= comp.q.len;   // behind the request: whatever is there
+                    vs[ng][w] = gone ? 0.f : p.x;
+                    vl[ng][w] = gone ? 0.f : fmaf(8.f, p.x, p.y);
+                    up |= vs[ng][w] > sref;
+                }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) up |= s[nt][e] > m[nt][e & 1] + kJump;
+            if (__any_sync(~0u, up)) {
+                // Move the references: rare after a request's first granules.
+                float top = 0.f;
+#pragma unroll
+                for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) top = fmaxf(top, vs[ng][w] < INFINITY ? vs[ng][w] : 0.f);
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                float ratio = 1.f;   // old sref over new
+                if (top > sref) {
+                    // the next power of two above (steps that are not finite only reach the columns that see them)
+                    const float n = __uint_as_float((__float_as_uint(top) & 0x7f800000u) + 0x00800000u);
+                    ratio = sref / n;
+                    sref = n;
+                    rs = (float)(1 << kShift) / n;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float t = fmaxf(s[nt][e], s[nt][2 + e]);
+                        t = fmaxf(t, __shfl_xor_sync(~0u, t, 4));
+                        t = fmaxf(t, __shfl_xor_sync(~0u, t, 8));
+                        t = fmaxf(t, __shfl_xor_sync(~0u, t, 16));
+                        const float n = fmaxf(m[nt][e], t);
+                        const float f = m[nt][e] == n ? 1.f : ex2(m[nt][e] - n);   // n above -inf where they differ
+                        m[nt][e] = n;
+                        l[nt][e] *= f;
+#pragma unroll
+                        for (int ng = 0; ng < NG; ++ng) {
+                            om[nt][ng][e] *= f;
+#pragma unroll
+                            for (int mt = 0; mt < 4; ++mt) {
+                                o[nt][ng][mt][e] *= f * ratio;
+                                o[nt][ng][mt][2 + e] *= f * ratio;
+                            }
+                        }
+                    }
+            }
+            // Weights, their sums, and the B operands p * step of the second product.
+            uint32_t pb[NT][NG][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float ref = m[nt][e & 1];
+                    p[e] = ex2(s[nt][e] - (ref == -INFINITY ? 0.f : ref));
+                    l[nt][e & 1] += p[e];
+                }
+#pragma unroll
+                for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        float x0 = p[2 * w] * (vs[ng][w] * rs), x1 = p[2 * w + 1] * (vs[ng][w] * rs);
+                        float y0 = p[2 * w] * vl[ng][w], y1 = p[2 * w + 1] * vl[ng][w];
+                        if (edge) {   // a masked token does not count, even one that is not finite
+                            if (s[nt][2 * w] == -INFINITY) x0 = y0 = 0.f;
+                            if (s[nt][2 * w + 1] == -INFINITY) x1 = y1 = 0.f;
+                        }
+                        om[nt][ng][0] += y0;
+                        om[nt][ng][1] += y1;
+                        pb[nt][ng][w] = mov_trans(pack_h2(x0, x1));
+                    }
+            }
+            // O^T += V^T P^T: a thread's tokens are those of operand columns 2 t4, 2 t4 + 1 and 8 above.
+            const int ta = 2 * t4 + (t4 & 1), tb = 2 * t4 + 1 - (t4 & 1);
+#pragma unroll
+            for (int ng = 0; ng < NG; ++ng) {
+                const unsigned char *v = st + HB + 32 * ng + 4 * g;
+                uint32_t lo[2][4], hi[2][4];
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const uint32_t x = *reinterpret_cast<const uint32_t *>(v + (ta + 8 * w) * (DIM / 2));
+                    const uint32_t y = *reinterpret_cast<const uint32_t *>(v + (tb + 8 * w) * (DIM / 2));
+                    unpack_h(__byte_perm(x, y, 0x5410), lo[w]);   // dimensions 8 g + 0 .. 3 of both tokens
+                    unpack_h(__byte_perm(x, y, 0x7632), hi[w]);   // 8 g + 4 .. 7
+                }
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) {
+                    const uint32_t(&z)[2][4] = mt < 2 ? lo : hi;
+                    const int i = 2 * (mt & 1);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma<false>(o[nt][ng][mt], z[0][i], z[0][i + 1], z[1][i], z[1][i + 1], pb[nt][ng][0], pb[nt][ng][1]);
+                }
+            }
+        }
+
+        // Join the warps.
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], d);
+#pragma unroll
+                    for (int ng = 0; ng < NG; ++ng) om[nt][ng][e] += __shfl_xor_sync(~0u, om[nt][ng][e], d);
+                }
+            }
+        __syncthreads();   // the buffers' last readers are done
+        const float unit = sref * (1.f / (1 << kShift));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int col = nt * 8 + 2 * t4 + e;
+                if (g == 0) {
+                    sm.m[warp][col] = m[nt][e];
+                    sm.l[warp][col] = l[nt][e];
+                }
+#pragma unroll
+                for (int ng = 0; ng < NG; ++ng) {
+                    float x[8];
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt) {   // rows g and g + 8 are dimensions 8 g + 2 mt and one above
+                        x[2 * mt] = fmaf(o[nt][ng][mt][e], unit, om[nt][ng][e]);
+                        x[2 * mt + 1] = fmaf(o[nt][ng][mt][2 + e], unit, om[nt][ng][e]);
+                    }
+                    float4 *d = reinterpret_cast<float4 *>(&sm.o[warp][col][64 * ng + 8 * g]);
+                    d[0] = make_float4(x[0], x[1], x[2], x[3]);
+                    d[1] = make_float4(x[4], x[5], x[6], x[7]);
+                }
+            }
+        __syncthreads();
+        const bool whole = comp.round == 0 && comp.n == comp.q.rounds;
+        const int slot = 2 * blockIdx.x + (first_piece && comp.round > 0 ? 0 : 1);
+        float *dst = part + (size_t)slot * partial_floats(DIM, NC);
+        constexpr int kChunks = DIM / 8;
+        for (int i = tid; i < NC * kChunks; i += kThreads) {
+            const int col = i / kChunks, d0 = (i % kChunks) * 8;
+            float mm = sm.m[0][col], ll = 0.f, x[8] = {};
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][col]);
+            const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = ex2(sm.m[w][col] - ref);
+                ll = fmaf(f, sm.l[w][col], ll);
+                const float4 u = *reinterpret_cast<const float4 *>(&sm.o[w][col][d0]);
+                const float4 v = *reinterpret_cast<const float4 *>(&sm.o[w][col][d0 + 4]);
+                x[0] = fmaf(f, u.x, x[0]); x[1] = fmaf(f, u.y, x[1]); x[2] = fmaf(f, u.z, x[2]); x[3] = fmaf(f, u.w, x[3]);
+                x[4] = fmaf(f, v.x, x[4]); x[5] = fmaf(f, v.y, x[5]); x[6] = fmaf(f, v.z, x[6]); x[7] = fmaf(f, v.w, x[7]);
+            }
+            if (!whole) {
+                float4 *p = reinterpret_cast<float4 *>(dst + col * DIM + d0);
+                p[0] = make_float4(x[0], x[1], x[2], x[3]);
+                p[1] = make_float4(x[4], x[5], x[6], x[7]);
+                if (d0 == 0) {
+                    dst[NC * DIM + col] = mm;
+                    dst[NC * DIM + NC + col] = ll;
+                }
+                continue;
+            }
+            const int gc = comp.ct * NC + col;
+            if (gc >= comp.q.nq * G) continue;
+            const int qi = gc / G, head = comp.h * G + gc - qi * G;
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
+            uint4 u;
+            H *e = reinterpret_cast<H *>(&u);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) e[k] = (H)(x[k] * inv);
+            *reinterpret_cast<uint4 *>(reinterpret_cast<H *>(a.o.p) + (long long)(comp.q.q0 + qi) * a.o.ts +
+                                       (long long)head * a.o.hs + d0) = u;
+            if (a.lse && d0 == 0)
+                a.lse[(size_t)(comp.q.q0 + qi) * a.hq + head] = ll == 0.f ? -INFINITY : 0.6931471805599453f * (ref + log2f(ll));
+        }
+        if (tid == 0 && !whole && comp.round + comp.n < comp.q.rounds && !(first_piece && comp.round > 0)) {
+            // the segment begins here and goes on: its last unit is u1 - 1 + (rounds not done)
+            const long long end = u1 - 1 + (comp.q.rounds - comp.round - comp.n);
+            long long last = ((end + 1) * ctas + total - 1) / total - 1;   // the CTA whose range holds `end`
+            while (total * (last + 1) / ctas <= end) ++last;
+            while (total * last / ctas > end) --last;
+            split[blockIdx.x] = Split{comp.r, comp.h, comp.ct, (int)last};
+        }
+        first_piece = false;
+        if (!comp.next(a, G)) break;
+    }
+    cp_wait<0>();
+}
+
+// Joins the pieces of the segment that begins in CTA blockIdx.x, in order.
+template <int DIM, int NT, bool BF>
+__global__ void __launch_bounds__(kThreads * kJoinGroups) kv_join_kernel(AttendArgs a, const Split *split, const float *part) {
+    using H = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+    constexpr int NC = 8 * NT, kChunks = DIM / 8;
+    __shared__ float sx[kJoinGroups][8][DIM], sl[kJoinGroups][8];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Split s = split[blockIdx.x];
+    if (s.last == 0) return;
+    const int G = a.hq / a.c.heads, first = blockIdx.x, n = s.last - first + 1;
+    const int grp = threadIdx.x / kThreads, tid = threadIdx.x % kThreads;
+    const int q0 = a.cu_q[s.r], nq = a.cu_q[s.r + 1] - q0;
+    // piece i: the second slot of the first CTA, the first slot of the others
+    const auto at = [&](int i) { return part + (size_t)(2 * (first + i) + (i == 0)) * partial_floats(DIM, NC); };
+    for (int nt = 0; nt < NT; ++nt) {
+        __syncthreads();
+        // kChunks = 16 (8): 128 threads are 8 (16, half of them idle) columns
+        const int col = tid / kChunks, d0 = (tid % kChunks) * 8, cc = nt * 8 + col;
+        float x[8] = {}, ll = 0.f, mm = -INFINITY;
+        if (col < 8) {
+            for (int i = 0; i < n; ++i) mm = fmaxf(mm, at(i)[NC * DIM + cc]);
+            const float ref = mm == -INFINITY ? 0.f : mm;
+            for (int i = grp; i < n; i += kJoinGroups) {
+                const float *p = at(i);
+                const float f = ex2(p[NC * DIM + cc] - ref);
+                ll = fmaf(f, p[NC * DIM + NC + cc], ll);
+                const float4 u = *reinterpret_cast<const float4 *>(p + cc * DIM + d0), v = *reinterpret_cast<const float4 *>(p + cc * DIM + d0 + 4);
+                x[0] = fmaf(f, u.x, x[0]); x[1] = fmaf(f, u.y, x[1]); x[2] = fmaf(f, u.z, x[2]); x[3] = fmaf(f, u.w, x[3]);
+                x[4] = fmaf(f, v.x, x[4]); x[5] = fmaf(f, v.y, x[5]); x[6] = fmaf(f, v.z, x[6]); x[7] = fmaf(f, v.w, x[7]);
+            }
+            for (int k = 0; k < 8; ++k) sx[grp][col][d0 + k] = x[k];
+            if (d0 == 0) sl[grp][col] = ll;
+        }
+        __syncthreads();
+        const int gc = s.ct * NC + cc;
+        if (grp != 0 || col >= 8 || gc >= nq * G) continue;
+        ll = 0.f;
+        for (int j = 0; j < kJoinGroups; ++j) ll += sl[j][col];
+        const int qi = gc / G, head = s.h * G + gc - qi * G;
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        uint4 u;
+        H *e = reinterpret_cast<H *>(&u);
+        for (int k = 0; k < 8; ++k) {
+            float y = 0.f;
+            for (int j = 0; j < kJoinGroups; ++j) y += sx[j][col][d0 + k];
+            e[k] = (H)(y * inv);
+        }
+        *reinterpret_cast<uint4 *>(reinterpret_cast<H *>(a.o.p) + (long long)(q0 + qi) * a.o.ts + (long long)head * a.o.hs + d0) = u;
+        if (a.lse && d0 == 0)
+            a.lse[(size_t)(q0 + qi) * a.hq + head] =
+                ll == 0.f ? -INFINITY : 0.6931471805599453f * ((mm == -INFINITY ? 0.f : mm) + log2f(ll));
+    }
+}
+
+int tiles_of(int hq, int hkv, int max_q) { return (long long)max_q * (hq / hkv) <= 8 ? 1 : 2; }
+
+constexpr size_t kSplitBytes = (kMaxCtas * sizeof(Split) + 255) / 256 * 256;
+
+template <int DIM, int NT, bool BF>
+int launch(const AttendArgs &a, cudaStream_t st) {
+    Split *split = static_cast<Split *>(a.ws);
+    float *part = reinterpret_cast<float *>(static_cast<char *>(a.ws) + kSplitBytes);
+    const size_t smem = sizeof(Smem<DIM, NT>);
+    if (int rc = cuda_check(cudaFuncSetAttribute(kv_attend_kernel<DIM, NT, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
+        return rc;
+    const int grid = NT == 1 ? kMaxCtas : kMaxCtas / 4 * 3;
+    kv_attend_kernel<DIM, NT, BF><<<grid, kThreads, smem, st>>>(a, split, part);
+    count_launch();
+    if (int rc = cuda_check(cudaGetLastError())) return rc;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads * kJoinGroups);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    count_launch();
+    return cuda_check(cudaLaunchKernelEx(&cfg, kv_join_kernel<DIM, NT, BF>, a, (const Split *)split, (const float *)part));
+}
+
+template <int DIM, int NT>
+int launch_type(const AttendArgs &a, cudaStream_t st) {
+    return a.dtype == LORA_BF16 ? launch<DIM, NT, true>(a, st) : launch<DIM, NT, false>(a, st);
+}
+
+}  // namespace
+
+size_t attend_workspace(int hq, int hkv, int dim, int max_q) {
+    const size_t n = partial_floats(dim, 8 * tiles_of(hq, hkv, max_q)) * 2 * kMaxCtas * sizeof(float);
+    return kSplitBytes + (n + 255) / 256 * 256;
+}
+
+int launch_kv_attend(const AttendArgs &a, cudaStream_t st) {
+    const bool one = tiles_of(a.hq, a.c.heads, a.max_q) == 1;
+    if (a.dim == 64) return one ? launch_type<64, 1>(a, st) : launch_type<64, 2>(a, st);
+    return one ? launch_type<128, 1>(a, st) : launch_type<128, 2>(a, st);
+}
+
+}  // namespace lora

@@ -11,38 +11,6 @@ constexpr int kWarps = 4;
 template <class H>
 __device__ __forceinline__ float to_f(H x) { return (float)x; }
 
-// Keys and values of a request from the cache.
-template <int DIM>
-struct CachedKv {
-    KvCache c;
-    const int32_t *table;
-    int h;
-    int32_t *err;
-    __device__ __forceinline__ bool at(int j, float (&k)[DIM / 32], float (&v)[DIM / 32]) const {
-        const int page = table[j / c.block], off = j % c.block, lane = threadIdx.x & 31;
-        if (page < 0 || page >= c.num_pages) {
-            if (err && lane == 0) atomicOr(err, LORA_DEV_ERR_BAD_PAGE);
-            return false;
-        }
-        const unsigned char *g = c.pages + page * c.page_bytes +
-                                 (long long)(h * c.granules + off / LORA_KV_GRANULE) * kv_granule_bytes(DIM);
-        const int row = off % LORA_KV_GRANULE;
-#pragma unroll
-        for (int i = 0; i < DIM / 32; ++i) {
-            const int d = lane * (DIM / 32) + i;
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const unsigned char *p = g + w * kv_half_bytes(DIM);
-                const int b = p[row * (DIM / 2) + d / 2];
-                const float2 s = __half22float2(
-                    reinterpret_cast<const __half2 *>(p + kv_code_bytes(DIM))[row * (DIM / LORA_KV_GROUP) + d / LORA_KV_GROUP]);
-                (w ? v : k)[i] = fmaf((float)((d & 1) ? b >> 4 : b & 15), s.x, s.y);
-            }
-        }
-        return true;
-    }
-};
-
 template <int DIM, class H>
 struct DenseKv {
     const H *kp, *vp;
@@ -98,25 +66,6 @@ __device__ __forceinline__ void attend_row(const Kv &kv, int n, const H *q, H *o
 }
 
 template <int DIM, class H>
-__global__ void __launch_bounds__(kWarps * 32) attend_cached_kernel(AttendArgs a) {
-    const int t = blockIdx.x, hq = blockIdx.y;
-    for (int r = 0; r < a.R; ++r) {
-        const int q0 = a.cu_q[r], q1 = a.cu_q[r + 1], n = q1 - q0, len = a.kv_len[r];
-        if (q0 == q1) continue;
-        if (q0 < 0 || q1 < q0 || q1 > a.T || n > a.max_q || len < 0 || (long long)len > (long long)a.max_blocks * a.c.block) {
-            if (a.err && threadIdx.x == 0 && t == 0 && hq == 0) atomicOr(a.err, LORA_DEV_ERR_BAD_LENGTH);
-            continue;
-        }
-        if (t < q0 || t >= q1) continue;
-        __syncthreads();
-        const CachedKv<DIM> kv{a.c, a.table + (size_t)r * a.max_blocks, hq / (a.hq / a.c.heads), a.err};
-        attend_row<DIM, H>(kv, len - n + (t - q0) + 1, reinterpret_cast<const H *>(a.q.p) + t * a.q.ts + hq * a.q.hs,
-                           reinterpret_cast<H *>(a.o.p) + t * a.o.ts + hq * a.o.hs,
-                           a.lse ? a.lse + (size_t)t * a.hq + hq : nullptr, a.scale);
-    }
-}
-
-template <int DIM, class H>
 __global__ void __launch_bounds__(kWarps * 32) attend_prompt_kernel(PromptArgs a) {
     const int t = blockIdx.x, hq = blockIdx.y, h = hq / (a.hq / a.hkv);
     for (int r = 0; r < a.R; ++r) {
@@ -137,18 +86,6 @@ __global__ void __launch_bounds__(kWarps * 32) attend_prompt_kernel(PromptArgs a
 }
 
 }  // namespace
-
-size_t attend_workspace(int, int, int, int) { return 256; }
-
-int launch_kv_attend(const AttendArgs &a, cudaStream_t st) {
-    const dim3 grid(a.T, a.hq);
-    if (a.dim == 64 && a.dtype == LORA_BF16) attend_cached_kernel<64, __nv_bfloat16><<<grid, kWarps * 32, 0, st>>>(a);
-    else if (a.dim == 64) attend_cached_kernel<64, __half><<<grid, kWarps * 32, 0, st>>>(a);
-    else if (a.dtype == LORA_BF16) attend_cached_kernel<128, __nv_bfloat16><<<grid, kWarps * 32, 0, st>>>(a);
-    else attend_cached_kernel<128, __half><<<grid, kWarps * 32, 0, st>>>(a);
-    count_launch();
-    return cuda_check(cudaGetLastError());
-}
 
 int launch_prompt(const PromptArgs &a, cudaStream_t st) {
     const dim3 grid(a.Tq, a.hq);
