@@ -173,19 +173,51 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                      "{%0, %1, %2, %3};" : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The masks and exponents of the unpacking, in registers: a mask-and-or with
+// two literals would take two instructions.
+struct Consts {
+    uint32_t lo, hi, h1024, b128, sixteenth;
+    __device__ __forceinline__ Consts() {
+        asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(lo));
+        asm volatile("mov.b32 %0, 0x00f000f0;" : "=r"(hi));
+        asm volatile("mov.b32 %0, 0x64006400;" : "=r"(h1024));
+        asm volatile("mov.b32 %0, 0x43004300;" : "=r"(b128));
+        asm volatile("mov.b32 %0, 0x2c002c00;" : "=r"(sixteenth));
+    }
+};
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(w), "r"(mask), "r"(bits));   // (w & mask) | bits
+    return y;
+}
+__device__ __forceinline__ uint32_t add_h2(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
 // Four fp16 pairs n - 8 from the fields of w: pair j holds fields j and j + 4.
-__device__ __forceinline__ void unpack_h(uint32_t w, uint32_t (&x)[4]) {
-    const uint32_t one = 0x3c003c00u, sub = 0xe408e408u /* -1032 */, sixteenth = 0x2c002c00u, sub72 = 0xd480d480u /* -72 */;
-    const uint32_t v = w >> 8;
-    x[0] = fma_h2((w & 0x000f000fu) | 0x64006400u, one, sub);
-    x[1] = fma_h2((w & 0x00f000f0u) | 0x64006400u, sixteenth, sub72);
-    x[2] = fma_h2((v & 0x000f000fu) | 0x64006400u, one, sub);
-    x[3] = fma_h2((v & 0x00f000f0u) | 0x64006400u, sixteenth, sub72);
+__device__ __forceinline__ void unpack_h(uint32_t w, uint32_t (&x)[4], const Consts &k) {
+    const uint32_t sub = 0xe408e408u /* -1032 */, sub72 = 0xd480d480u /* -72 */, v = w >> 8;
+    x[0] = add_h2(and_or(w, k.lo, k.h1024), sub);
+    x[1] = fma_h2(and_or(w, k.hi, k.h1024), k.sixteenth, sub72);
+    x[2] = add_h2(and_or(v, k.lo, k.h1024), sub);
+    x[3] = fma_h2(and_or(v, k.hi, k.h1024), k.sixteenth, sub72);
 }
 // Four bf16 pairs 128 + n.
-__device__ __forceinline__ void unpack_b(uint32_t w, uint32_t (&x)[4]) {
+__device__ __forceinline__ void unpack_b(uint32_t w, uint32_t (&x)[4], const Consts &k) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u;
+    for (int j = 0; j < 4; ++j) x[j] = and_or(w >> (4 * j), k.lo, k.b128);
+}
+// (step, low) of a token's groups.
+template <int NG>
+__device__ __forceinline__ void load_params(const unsigned char *p, float2 (&x)[NG]) {
+    if (NG == 2) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        x[0] = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
+        x[NG - 1] = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
+    } else {
+        x[0] = __half22float2(*reinterpret_cast<const __half2 *>(p));
+    }
 }
 
 template <int DIM, int NT, bool BF>
@@ -249,15 +281,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
     load = comp;
 
     // The warp's granules, in order, into its ring.
-    const uint32_t ring = ptx::smem_u32(sm.ring[warp]);
-    int lg = load.g0() + warp, lend = load.g1(), ids = 0, ids_from = lg;
+    const Consts kc;
+    const uint32_t ring = ptx::smem_u32(sm.ring[warp]) + lane * 16;
+    const unsigned char *pages = a.c.pages + lane * 16;
+    int lg = load.g0() + warp, lend = load.g1(), in_ids = 0;
+    long long where = 0;   // lane i: byte offset of the warp's granule i from the last fetch, -1: no page
     bool more = true;
-    uint32_t valid = 0;   // bit s: stage s holds a granule
+    uint32_t valid = 0;    // bit s: stage s holds a granule
     int in_slot = 0;
-    const auto fetch_ids = [&]() {   // table entries of the warp's next 32 granules of the piece
-        ids_from = lg;
-        const int gi = lg + kWarps * lane;
-        ids = gi < lend ? a.table[(size_t)load.r * a.max_blocks + gi / a.c.granules] : 0;
+    const auto fetch_ids = [&]() {   // the warp's next 32 granules of the piece
+        in_ids = 0;
+        const int gi = lg + kWarps * lane, blk = gi / a.c.granules;
+        if (gi < lend) {
+            const int page = a.table[(size_t)load.r * a.max_blocks + blk];
+            where = -1;
+            if (page >= 0 && page < a.c.num_pages)
+                where = page * a.c.page_bytes + (long long)(load.h * a.c.granules + gi - blk * a.c.granules) * GB;
+            else if (a.err)
+                atomicOr(a.err, LORA_DEV_ERR_BAD_PAGE);
+        }
     };
     const auto advance = [&]() {
         while (more && lg >= lend) {
@@ -272,21 +314,18 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
     const auto issue = [&]() {
         valid &= ~(1u << in_slot);
         if (more) {
-            if (lg - ids_from >= 32 * kWarps) fetch_ids();
-            const int page = __shfl_sync(~0u, ids, (lg - ids_from) / kWarps);
-            if (page >= 0 && page < a.c.num_pages) {
-                const unsigned char *src = a.c.pages + page * a.c.page_bytes +
-                                           (long long)(load.h * a.c.granules + lg % a.c.granules) * GB;
+            const long long off = __shfl_sync(~0u, where, in_ids);
+            if (off >= 0) {
+                const unsigned char *src = pages + off;
                 const uint32_t dst = ring + in_slot * GB;
 #pragma unroll
-                for (int i = 0; i < GB / 512; ++i) cp16(dst + (lane + 32 * i) * 16, src + (lane + 32 * i) * 16);
-                if (lane < GB % 512 / 16) cp16(dst + (lane + GB / 512 * 32) * 16, src + (lane + GB / 512 * 32) * 16);
+                for (int i = 0; i < GB / 512; ++i) cp16(dst + 512 * i, src + 512 * i);
+                if (lane < GB % 512 / 16) cp16(dst + GB / 512 * 512, src + GB / 512 * 512);
                 valid |= 1u << in_slot;
-            } else if (lane == 0 && a.err) {
-                atomicOr(a.err, LORA_DEV_ERR_BAD_PAGE);
             }
             lg += kWarps;
-            advance();
+            if (lg >= lend) advance();
+            else if (++in_ids == 32) fetch_ids();
         }
         cp_commit();
         in_slot = in_slot + 1 == kStages ? 0 : in_slot + 1;
@@ -296,7 +335,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue();
 
-    const float c = a.scale * 1.4426950408889634f;
+    // Scores stay as step * (q . n) + ... until the exponential, which takes them times c (>= 0: a negative scale
+    // turns the queries' signs).
+    const float c = fabsf(a.scale) * 1.4426950408889634f, jump = kJump / c;
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
     const int tok = g ^ ((g >> 1) & 1);   // token (of 8) in the operands' row g: both tokens of a pair on different banks
     int out_slot = 0;
     bool first_piece = true;
@@ -318,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
                 for (int i = 0; i < 2; ++i) {
                     uint4 u = make_uint4(0, 0, 0, 0);
                     if (ok) u = *reinterpret_cast<const uint4 *>(row + 64 * ng + 16 * t4 + 8 * i);
+                    u.x ^= flip; u.y ^= flip; u.z ^= flip; u.w ^= flip;
                     const H *e = reinterpret_cast<const H *>(&u);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) sum += (float)e[j];
@@ -341,9 +384,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
 #pragma unroll
             for (int e = 0; e < 2; ++e) lim[nt][e] = back + min(comp.q.nq - 1, (comp.ct * NC + nt * 8 + 2 * t4 + e) / G);
 
-        float o[NT][NG][4][4] = {}, om[NT][NG][2] = {}, l[NT][2] = {}, m[NT][2];
+        float o[NT][NG][4][4] = {}, om[NT][NG][2] = {}, l[NT][2] = {};
+        float m[NT][2], mc[NT][2], thr[NT][2];   // reference score (-inf: none yet); it times c (0); the score that moves it
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[nt][e] = thr[nt][e] = -INFINITY;
+                mc[nt][e] = 0.f;
+            }
         float sref = 0.f, rs = 0.f;   // largest step so far as a power of two; 2^kShift over it
 
         const int gend = comp.g1();
@@ -366,11 +415,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
                 for (int i = 0; i < 2; ++i) {
                     uint32_t x[4], y[4];
                     if (BF) {
-                        unpack_b(i ? w0.y : w0.x, x);
-                        unpack_b(i ? w1.y : w1.x, y);
+                        unpack_b(i ? w0.y : w0.x, x, kc);
+                        unpack_b(i ? w1.y : w1.x, y, kc);
                     } else {
-                        unpack_h(i ? w0.y : w0.x, x);
-                        unpack_h(i ? w1.y : w1.x, y);
+                        unpack_h(i ? w0.y : w0.x, x, kc);
+                        unpack_h(i ? w1.y : w1.x, y, kc);
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -380,19 +429,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
                     }
                 }
             }
-            // Scores in powers of two.
-            float s[NT][4] = {};
+            // Scores.
+            float s[NT][4];
 #pragma unroll
-            for (int ng = 0; ng < NG; ++ng) {
+            for (int w = 0; w < 2; ++w) {
+                float2 p[NG];
+                load_params<NG>(st + CB + (tok + 8 * w) * 4 * NG, p);
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(st + CB + (tok + 8 * w) * 4 * NG + 4 * ng));
-                    const float sc = p.x * c, lc = fmaf(BF ? -128.f : 8.f, sc, p.y * c);
+                for (int ng = 0; ng < NG; ++ng) {
+                    const float low = fmaf(BF ? -128.f : 8.f, p[ng].x, p[ng].y);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            s[nt][2 * w + e] = fmaf(sc, acc[nt][ng][2 * w + e], fmaf(lc, qs[nt][ng][e], s[nt][2 * w + e]));
+                        for (int e = 0; e < 2; ++e) {
+                            const float x = ng == 0 ? low * qs[nt][0][e] : fmaf(low, qs[nt][ng][e], s[nt][2 * w + e]);
+                            s[nt][2 * w + e] = fmaf(p[ng].x, acc[nt][ng][2 * w + e], x);
+                        }
                 }
             }
             const int j0 = gi * LORA_KV_GRANULE;
@@ -405,22 +457,24 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
                         if (j0 + tok + 8 * (e >> 1) > lim[nt][e & 1]) s[nt][e] = -INFINITY;
             }
             // Steps and lows of the values.
-            float vs[NG][2], vl[NG][2];
-            bool up = false;
+            float vs[NG][2], vl[NG][2], most = 0.f;
 #pragma unroll
-            for (int ng = 0; ng < NG; ++ng)
+            for (int w = 0; w < 2; ++w) {
+                float2 p[NG];
+                load_params<NG>(st + HB + CB + (tok + 8 * w) * 4 * NG, p);
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(st + HB + CB + (tok + 8 * w) * 4 * NG + 4 * ng));
-                    const bool gone = edge && j0 + tok + 8 * w >= comp.q.len;   // behind the request: whatever is there
-                    vs[ng][w] = gone ? 0.f : p.x;
-                    vl[ng][w] = gone ? 0.f : fmaf(8.f, p.x, p.y);
-                    up |= vs[ng][w] > sref;
+                for (int ng = 0; ng < NG; ++ng) {
+                    vs[ng][w] = p[ng].x;
+                    vl[ng][w] = fmaf(8.f, p[ng].x, p[ng].y);
+                    if (edge && j0 + tok + 8 * w >= comp.q.len) vs[ng][w] = vl[ng][w] = 0.f;   // behind the request: whatever is there
+                    most = fmaxf(most, vs[ng][w]);
                 }
+            }
+            bool up = most > sref;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) up |= s[nt][e] > m[nt][e & 1] + kJump;
+                for (int e = 0; e < 2; ++e) up |= fmaxf(s[nt][e], s[nt][2 + e]) > thr[nt][e];
             if (__any_sync(~0u, up)) {
                 // Move the references: rare after a request's first granules.
                 float top = 0.f;
@@ -447,8 +501,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
                         t = fmaxf(t, __shfl_xor_sync(~0u, t, 8));
                         t = fmaxf(t, __shfl_xor_sync(~0u, t, 16));
                         const float n = fmaxf(m[nt][e], t);
-                        const float f = m[nt][e] == n ? 1.f : ex2(m[nt][e] - n);   // n above -inf where they differ
+                        const float f = m[nt][e] == n ? 1.f : m[nt][e] == -INFINITY ? 0.f : ex2((m[nt][e] - n) * c);
                         m[nt][e] = n;
+                        mc[nt][e] = n == -INFINITY ? 0.f : n * c;
+                        thr[nt][e] = n + jump;
                         l[nt][e] *= f;
 #pragma unroll
                         for (int ng = 0; ng < NG; ++ng) {
@@ -468,15 +524,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
                 float p[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float ref = m[nt][e & 1];
-                    p[e] = ex2(s[nt][e] - (ref == -INFINITY ? 0.f : ref));
+                    p[e] = ex2(fmaf(s[nt][e], c, -mc[nt][e & 1]));
+                    if (edge && s[nt][e] == -INFINITY) p[e] = 0.f;   // with scale 0 too
                     l[nt][e & 1] += p[e];
                 }
 #pragma unroll
                 for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
-                        float x0 = p[2 * w] * (vs[ng][w] * rs), x1 = p[2 * w + 1] * (vs[ng][w] * rs);
+                        const float vr = vs[ng][w] * rs;
+                        float x0 = p[2 * w] * vr, x1 = p[2 * w + 1] * vr;
                         float y0 = p[2 * w] * vl[ng][w], y1 = p[2 * w + 1] * vl[ng][w];
                         if (edge) {   // a masked token does not count, even one that is not finite
                             if (s[nt][2 * w] == -INFINITY) x0 = y0 = 0.f;
@@ -497,8 +554,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
                 for (int w = 0; w < 2; ++w) {
                     const uint32_t x = *reinterpret_cast<const uint32_t *>(v + (ta + 8 * w) * (DIM / 2));
                     const uint32_t y = *reinterpret_cast<const uint32_t *>(v + (tb + 8 * w) * (DIM / 2));
-                    unpack_h(__byte_perm(x, y, 0x5410), lo[w]);   // dimensions 8 g + 0 .. 3 of both tokens
-                    unpack_h(__byte_perm(x, y, 0x7632), hi[w]);   // 8 g + 4 .. 7
+                    unpack_h(__byte_perm(x, y, 0x5410), lo[w], kc);   // dimensions 8 g + 0 .. 3 of both tokens
+                    unpack_h(__byte_perm(x, y, 0x7632), hi[w], kc);   // 8 g + 4 .. 7
                 }
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) {
@@ -531,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
             for (int e = 0; e < 2; ++e) {
                 const int col = nt * 8 + 2 * t4 + e;
                 if (g == 0) {
-                    sm.m[warp][col] = m[nt][e];
+                    sm.m[warp][col] = m[nt][e] == -INFINITY ? -INFINITY : mc[nt][e];
                     sm.l[warp][col] = l[nt][e];
                 }
 #pragma unroll
