@@ -50,9 +50,9 @@ namespace lora {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kRound = kWarps * LORA_KV_GRANULE;   // tokens of a unit
-constexpr int kMaxCtas = 592;                      // 4 CTAs on each of 148 SMs
-constexpr int kStages = 4;
+constexpr int kMaxCtas = 444;                      // 3 CTAs on each of 148 SMs
+constexpr int kStages = 3;
+constexpr int kFixed = 2;                          // units that starting and joining a segment costs beside its rounds
 constexpr float kJump = 10.f;                      // log2 by which a score may exceed the reference
 constexpr int kShift = 5;                          // weights are scaled by 2^kShift in fp16
 constexpr int kJoinGroups = 4;                     // thread groups of the joining kernel
@@ -62,9 +62,9 @@ struct Split {
     int r, h, ct, last;   // last = 0: none
 };
 
-template <int DIM, int NT>
+template <int DIM, int NT, int U>
 struct Smem {
-    alignas(128) unsigned char ring[kWarps][kStages][kv_granule_bytes(DIM)];
+    alignas(128) unsigned char ring[kWarps][kStages][U * kv_granule_bytes(DIM)];
     float o[kWarps][8 * NT][DIM + 4];
     float m[kWarps][8 * NT], l[kWarps][8 * NT];
     long long scan[kWarps];
@@ -78,7 +78,8 @@ struct Req {
     int q0, nq, len, rounds, tiles;
 };
 
-template <int NC>
+// ROUND: granules the CTA's warps take at a time.
+template <int NC, int ROUND>
 __device__ __forceinline__ Req load_req(const AttendArgs &a, int r, int G, bool &bad) {
     Req q;
     q.q0 = a.cu_q[r];
@@ -89,48 +90,56 @@ __device__ __forceinline__ Req load_req(const AttendArgs &a, int r, int G, bool 
                          (long long)q.len > (long long)a.max_blocks * a.c.block);
     if (bad || q1 == q.q0) q.nq = 0;
     q.tiles = (q.nq * G + NC - 1) / NC;
-    q.rounds = q.len <= 0 ? 1 : (q.len + kRound - 1) / kRound;
+    constexpr int tokens = ROUND * LORA_KV_GRANULE;
+    q.rounds = q.len <= 0 ? 1 : (q.len + tokens - 1) / tokens;
     return q;
 }
 
+// Units of a request: every (head, tile) is kFixed units and its rounds.
+__device__ __forceinline__ long long units_of(const Req &q, int heads) {
+    return (long long)q.tiles * heads * (q.rounds + kFixed);
+}
+
 // A walk over this CTA's pieces in order.
-template <int NC>
+template <int NC, int ROUND>
 struct Walk {
     Req q;
-    int r, h, ct, round, n;   // current piece: rounds [round, round + n) of (r, h, ct)
+    int r, h, ct, round, n;   // current piece: rounds [round, round + n) of (r, h, ct); n = 0 only right after start()
     long long left;           // units after this piece
     __device__ __forceinline__ void start(const AttendArgs &a, int G, int r0, long long off, long long units) {
         r = r0;
         bool bad;
-        q = load_req<NC>(a, r, G, bad);
-        const long long seg = off / q.rounds;
-        round = (int)(off - seg * q.rounds);
+        q = load_req<NC, ROUND>(a, r, G, bad);
+        const int all = q.rounds + kFixed;
+        const long long seg = off / all;
+        const int from = (int)(off - seg * all), to = (int)min((long long)all, from + units);
         h = (int)(seg / q.tiles);
         ct = (int)(seg - (long long)h * q.tiles);
-        n = (int)min((long long)(q.rounds - round), units);
-        left = units - n;
+        round = max(0, from - kFixed);
+        n = max(0, to - kFixed) - round;
+        left = units - (to - from);
     }
     __device__ __forceinline__ bool next(const AttendArgs &a, int G) {
-        if (left == 0) return false;
+        if (left <= kFixed) return false;   // none, or not one round of the next segment
         round = 0;
         if (++ct == q.tiles) {
             ct = 0;
             if (++h == a.c.heads) {
                 h = 0;
                 bool bad;
-                do q = load_req<NC>(a, ++r, G, bad);
+                do q = load_req<NC, ROUND>(a, ++r, G, bad);
                 while (q.nq == 0);
             }
         }
-        n = (int)min((long long)q.rounds, left);
-        left -= n;
+        n = (int)min((long long)q.rounds, left - kFixed);
+        left -= n + kFixed;
         return true;
     }
     // granules of the piece: [g0, g1)
-    __device__ __forceinline__ int g0() const { return round * kWarps; }
+    __device__ __forceinline__ int g0() const { return round * ROUND; }
     __device__ __forceinline__ int g1() const {
         const int all = q.len <= 0 ? 0 : (q.len + LORA_KV_GRANULE - 1) / LORA_KV_GRANULE;
-        return min(all, (round + n) * kWarps);
+        return min(all, (round + n) * ROUND);
     }
 };
 
@@ -172,6 +181,18 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                      "{%0, %1, %2, %3};" : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d = a b
+template <bool BF>
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    if (BF)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%10, %10, %10, %10};" : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%10, %10, %10, %10};" : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // The masks and exponents of the unpacking, in registers: a mask-and-or with
 // two literals would take two instructions.
@@ -220,12 +241,13 @@ __device__ __forceinline__ void load_params(const unsigned char *p, float2 (&x)[
     }
 }
 
-template <int DIM, int NT, bool BF>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(AttendArgs a, Split *split, float *part) {
+template <int DIM, int NT, int U, bool BF>
+__global__ void __launch_bounds__(kThreads, 3) kv_attend_kernel(AttendArgs a, Split *split, float *part) {
     using H = typename std::conditional<BF, __nv_bfloat16, __half>::type;
     constexpr int NC = 8 * NT, NG = DIM / LORA_KV_GROUP, GB = kv_granule_bytes(DIM), HB = kv_half_bytes(DIM), CB = kv_code_bytes(DIM);
+    constexpr int ROUND = kWarps * U;
     extern __shared__ unsigned char smem_raw[];
-    Smem<DIM, NT> &sm = *reinterpret_cast<Smem<DIM, NT> *>(smem_raw);
+    Smem<DIM, NT, U> &sm = *reinterpret_cast<Smem<DIM, NT, U> *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int G = a.hq / a.c.heads;
 
@@ -235,8 +257,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
     bool any_bad = false;
     for (int r = ra; r < rb; ++r) {
         bool bad;
-        const Req q = load_req<NC>(a, r, G, bad);
-        mine += (long long)q.tiles * q.rounds * a.c.heads;
+        mine += units_of(load_req<NC, ROUND>(a, r, G, bad), a.c.heads);
         any_bad |= bad;
     }
     if (any_bad && blockIdx.x == 0 && a.err) atomicOr(a.err, LORA_DEV_ERR_BAD_LENGTH);
@@ -258,17 +279,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
     const long long ctas = min((long long)gridDim.x, total);
     const long long u0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
     const long long u1 = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : total;
-    if (u0 >= u1) {
-        if (tid == 0) split[blockIdx.x].last = 0;
-        return;
-    }
+    if (tid == 0) split[blockIdx.x].last = 0;
+    if (u0 >= u1) return;
     if (run <= u0 && u0 < run + mine) {
         long long base = run;
         int r = ra;
         for (;; ++r) {
             bool bad;
-            const Req q = load_req<NC>(a, r, G, bad);
-            const long long n = (long long)q.tiles * q.rounds * a.c.heads;
+            const long long n = units_of(load_req<NC, ROUND>(a, r, G, bad), a.c.heads);
             if (u0 < base + n) break;
             base += n;
         }
@@ -276,25 +294,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
         sm.base = base;
     }
     __syncthreads();
-    Walk<NC> load, comp;
+    Walk<NC, ROUND> load, comp;
     comp.start(a, G, sm.first, u0 - sm.base, u1 - u0);
+    if (comp.n == 0 && !comp.next(a, G)) return;
     load = comp;
 
-    // The warp's granules, in order, into its ring.
+    // The warp's granules, U at a time, into its ring.
     const Consts kc;
     const uint32_t ring = ptx::smem_u32(sm.ring[warp]) + lane * 16;
     const unsigned char *pages = a.c.pages + lane * 16;
-    int lg = load.g0() + warp, lend = load.g1(), in_ids = 0;
-    long long where = 0;   // lane i: byte offset of the warp's granule i from the last fetch, -1: no page
+    int lg = load.g0() + U * warp, lend = load.g1(), in_ids = 0;
+    long long where = -1;   // lane i: byte offset of the i-th granule the warp loads from the last fetch on, -1: none
     bool more = true;
-    uint32_t valid = 0;    // bit s: stage s holds a granule
+    uint32_t valid = 0;     // bits s U .. s U + U - 1: the granules that stage s holds
     int in_slot = 0;
     const auto fetch_ids = [&]() {   // the warp's next 32 granules of the piece
         in_ids = 0;
-        const int gi = lg + kWarps * lane, blk = gi / a.c.granules;
+        const int gi = lg + ROUND * (lane / U) + lane % U, blk = gi / a.c.granules;
+        where = -1;
         if (gi < lend) {
             const int page = a.table[(size_t)load.r * a.max_blocks + blk];
-            where = -1;
             if (page >= 0 && page < a.c.num_pages)
                 where = page * a.c.page_bytes + (long long)(load.h * a.c.granules + gi - blk * a.c.granules) * GB;
             else if (a.err)
@@ -305,27 +324,32 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
         while (more && lg >= lend) {
             more = load.next(a, G);
             if (more) {
-                lg = load.g0() + warp;
+                lg = load.g0() + U * warp;
                 lend = load.g1();
                 if (lg < lend) fetch_ids();
             }
         }
     };
     const auto issue = [&]() {
-        valid &= ~(1u << in_slot);
         if (more) {
-            const long long off = __shfl_sync(~0u, where, in_ids);
-            if (off >= 0) {
-                const unsigned char *src = pages + off;
-                const uint32_t dst = ring + in_slot * GB;
+            uint32_t bits = 0;
 #pragma unroll
-                for (int i = 0; i < GB / 512; ++i) cp16(dst + 512 * i, src + 512 * i);
-                if (lane < GB % 512 / 16) cp16(dst + GB / 512 * 512, src + GB / 512 * 512);
-                valid |= 1u << in_slot;
+            for (int u = 0; u < U; ++u) {
+                const long long off = __shfl_sync(~0u, where, in_ids + u);
+                if (off >= 0) {
+                    const unsigned char *src = pages + off;
+                    const uint32_t dst = ring + (in_slot * U + u) * GB;
+#pragma unroll
+                    for (int i = 0; i < GB / 512; ++i) cp16(dst + 512 * i, src + 512 * i);
+                    if (lane < GB % 512 / 16) cp16(dst + GB / 512 * 512, src + GB / 512 * 512);
+                    bits |= 1u << u;
+                }
             }
-            lg += kWarps;
+            valid = (valid & ~(((1u << U) - 1) << (in_slot * U))) | bits << (in_slot * U);
+            lg += ROUND;
+            in_ids += U;
             if (lg >= lend) advance();
-            else if (++in_ids == 32) fetch_ids();
+            else if (in_ids == 32) fetch_ids();
         }
         cp_commit();
         in_slot = in_slot + 1 == kStages ? 0 : in_slot + 1;
@@ -342,7 +366,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
     const int tok = g ^ ((g >> 1) & 1);   // token (of 8) in the operands' row g: both tokens of a pair on different banks
     int out_slot = 0;
     bool first_piece = true;
-    if (tid == 0) split[blockIdx.x].last = 0;
     for (;;) {
         // Queries of this piece: fragments, and per group their sums.
         uint32_t qf[NT][NG][4][2];
@@ -395,93 +418,100 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
             }
         float sref = 0.f, rs = 0.f;   // largest step so far as a power of two; 2^kShift over it
 
-        const int gend = comp.g1();
-        for (int gi = comp.g0() + warp; gi < gend; gi += kWarps) {
-            cp_wait<kStages - 2>();
-            __syncwarp();
-            issue();
-            const bool here = (valid >> out_slot) & 1;
-            const unsigned char *st = sm.ring[warp][out_slot];
-            out_slot = out_slot + 1 == kStages ? 0 : out_slot + 1;
-            if (!here) continue;
-
-            // S^T = K Q^T: rows g and g + 8 of the operand are tokens tok and tok + 8.
-            float acc[NT][NG][4] = {};
+        // U granules at `st`, the first of them granule gi of the request. EDGE: some are missing (`bits`) or hold masked tokens.
+        const auto step = [&](auto edge, const unsigned char *st, int gi, uint32_t bits) {
+            constexpr bool EDGE = decltype(edge)::value;
+            float s[U][NT][4];
 #pragma unroll
-            for (int ng = 0; ng < NG; ++ng) {
-                const uint2 w0 = *reinterpret_cast<const uint2 *>(st + tok * (DIM / 2) + 32 * ng + 8 * t4);
-                const uint2 w1 = *reinterpret_cast<const uint2 *>(st + (tok + 8) * (DIM / 2) + 32 * ng + 8 * t4);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t x[4], y[4];
-                    if (BF) {
-                        unpack_b(i ? w0.y : w0.x, x, kc);
-                        unpack_b(i ? w1.y : w1.x, y, kc);
-                    } else {
-                        unpack_h(i ? w0.y : w0.x, x, kc);
-                        unpack_h(i ? w1.y : w1.x, y, kc);
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        // fields (0, 4) and (1, 5) against dimensions 0, 4 and 1, 5; then (2, 6) and (3, 7)
-                        mma<BF>(acc[nt][ng], x[0], y[0], x[1], y[1], qf[nt][ng][2 * i][0], qf[nt][ng][2 * i][1]);
-                        mma<BF>(acc[nt][ng], x[2], y[2], x[3], y[3], qf[nt][ng][2 * i + 1][0], qf[nt][ng][2 * i + 1][1]);
-                    }
-                }
-            }
-            // Scores.
-            float s[NT][4];
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                float2 p[NG];
-                load_params<NG>(st + CB + (tok + 8 * w) * 4 * NG, p);
+            for (int u = 0; u < U; ++u) {
+                const unsigned char *k = st + u * GB;
+                // S^T = K Q^T: rows g and g + 8 of the operand are tokens tok and tok + 8.
+                float acc[NT][NG][4];
 #pragma unroll
                 for (int ng = 0; ng < NG; ++ng) {
-                    const float low = fmaf(BF ? -128.f : 8.f, p[ng].x, p[ng].y);
+                    const uint2 w0 = *reinterpret_cast<const uint2 *>(k + tok * (DIM / 2) + 32 * ng + 8 * t4);
+                    const uint2 w1 = *reinterpret_cast<const uint2 *>(k + (tok + 8) * (DIM / 2) + 32 * ng + 8 * t4);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float x = ng == 0 ? low * qs[nt][0][e] : fmaf(low, qs[nt][ng][e], s[nt][2 * w + e]);
-                            s[nt][2 * w + e] = fmaf(p[ng].x, acc[nt][ng][2 * w + e], x);
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t x[4], y[4];
+                        if (BF) {
+                            unpack_b(i ? w0.y : w0.x, x, kc);
+                            unpack_b(i ? w1.y : w1.x, y, kc);
+                        } else {
+                            unpack_h(i ? w0.y : w0.x, x, kc);
+                            unpack_h(i ? w1.y : w1.x, y, kc);
                         }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            // fields (0, 4) and (1, 5) against dimensions 0, 4 and 1, 5; then (2, 6) and (3, 7)
+                            if (i == 0) mma_first<BF>(acc[nt][ng], x[0], y[0], x[1], y[1], qf[nt][ng][0][0], qf[nt][ng][0][1]);
+                            else mma<BF>(acc[nt][ng], x[0], y[0], x[1], y[1], qf[nt][ng][2][0], qf[nt][ng][2][1]);
+                            mma<BF>(acc[nt][ng], x[2], y[2], x[3], y[3], qf[nt][ng][2 * i + 1][0], qf[nt][ng][2 * i + 1][1]);
+                        }
+                    }
                 }
-            }
-            const int j0 = gi * LORA_KV_GRANULE;
-            const bool edge = j0 + LORA_KV_GRANULE - 1 > least;
-            if (edge) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int w = 0; w < 2; ++w) {
+                    float2 p[NG];
+                    load_params<NG>(k + CB + (tok + 8 * w) * 4 * NG, p);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (j0 + tok + 8 * (e >> 1) > lim[nt][e & 1]) s[nt][e] = -INFINITY;
+                    for (int ng = 0; ng < NG; ++ng) {
+                        const float low = fmaf(BF ? -128.f : 8.f, p[ng].x, p[ng].y);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float x = ng == 0 ? low * qs[nt][0][e] : fmaf(low, qs[nt][ng][e], s[u][nt][2 * w + e]);
+                                s[u][nt][2 * w + e] = fmaf(p[ng].x, acc[nt][ng][2 * w + e], x);
+                            }
+                    }
+                    if (EDGE) {
+                        const int j = (gi + u) * LORA_KV_GRANULE + tok + 8 * w;
+                        const bool here = (bits >> u) & 1;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (!here || j > lim[nt][e]) s[u][nt][2 * w + e] = -INFINITY;
+                    }
+                }
             }
             // Steps and lows of the values.
-            float vs[NG][2], vl[NG][2], most = 0.f;
+            float vs[U][NG][2], vl[U][NG][2], most = 0.f;
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                float2 p[NG];
-                load_params<NG>(st + HB + CB + (tok + 8 * w) * 4 * NG, p);
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int ng = 0; ng < NG; ++ng) {
-                    vs[ng][w] = p[ng].x;
-                    vl[ng][w] = fmaf(8.f, p[ng].x, p[ng].y);
-                    if (edge && j0 + tok + 8 * w >= comp.q.len) vs[ng][w] = vl[ng][w] = 0.f;   // behind the request: whatever is there
-                    most = fmaxf(most, vs[ng][w]);
+                for (int w = 0; w < 2; ++w) {
+                    float2 p[NG];
+                    load_params<NG>(st + u * GB + HB + CB + (tok + 8 * w) * 4 * NG, p);
+#pragma unroll
+                    for (int ng = 0; ng < NG; ++ng) {
+                        vs[u][ng][w] = p[ng].x;
+                        vl[u][ng][w] = fmaf(8.f, p[ng].x, p[ng].y);
+                        if (EDGE && (!((bits >> u) & 1) || (gi + u) * LORA_KV_GRANULE + tok + 8 * w >= comp.q.len))
+                            vs[u][ng][w] = vl[u][ng][w] = 0.f;   // not the request's: whatever is there
+                        most = fmaxf(most, vs[u][ng][w]);
+                    }
                 }
-            }
             bool up = most > sref;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) up |= fmaxf(s[nt][e], s[nt][2 + e]) > thr[nt][e];
+                for (int e = 0; e < 2; ++e) {
+                    float t = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+#pragma unroll
+                    for (int u = 1; u < U; ++u) t = fmaxf(t, fmaxf(s[u][nt][e], s[u][nt][2 + e]));
+                    up |= t > thr[nt][e];
+                }
             if (__any_sync(~0u, up)) {
                 // Move the references: rare after a request's first granules.
                 float top = 0.f;
 #pragma unroll
-                for (int ng = 0; ng < NG; ++ng)
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) top = fmaxf(top, vs[ng][w] < INFINITY ? vs[ng][w] : 0.f);
+                    for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) top = fmaxf(top, vs[u][ng][w] < INFINITY ? vs[u][ng][w] : 0.f);
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
                 float ratio = 1.f;   // old sref over new
@@ -496,7 +526,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float t = fmaxf(s[nt][e], s[nt][2 + e]);
+                        float t = -INFINITY;
+#pragma unroll
+                        for (int u = 0; u < U; ++u) t = fmaxf(t, fmaxf(s[u][nt][e], s[u][nt][2 + e]));
                         t = fmaxf(t, __shfl_xor_sync(~0u, t, 4));
                         t = fmaxf(t, __shfl_xor_sync(~0u, t, 8));
                         t = fmaxf(t, __shfl_xor_sync(~0u, t, 16));
@@ -517,55 +549,70 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv_attend_kernel(At
                         }
                     }
             }
-            // Weights, their sums, and the B operands p * step of the second product.
-            uint32_t pb[NT][NG][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float p[4];
+            for (int u = 0; u < U; ++u) {
+                // Weights, their sums, and the B operands p * step of the second product.
+                uint32_t pb[NT][NG][2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    p[e] = ex2(fmaf(s[nt][e], c, -mc[nt][e & 1]));
-                    if (edge && s[nt][e] == -INFINITY) p[e] = 0.f;   // with scale 0 too
-                    l[nt][e & 1] += p[e];
+                for (int nt = 0; nt < NT; ++nt) {
+                    float p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        p[e] = ex2(fmaf(s[u][nt][e], c, -mc[nt][e & 1]));
+                        if (EDGE && s[u][nt][e] == -INFINITY) p[e] = 0.f;   // with scale 0 too
+                        l[nt][e & 1] += p[e];
+                    }
+#pragma unroll
+                    for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            const float vr = vs[u][ng][w] * rs;
+                            float x0 = p[2 * w] * vr, x1 = p[2 * w + 1] * vr;
+                            float y0 = p[2 * w] * vl[u][ng][w], y1 = p[2 * w + 1] * vl[u][ng][w];
+                            if (EDGE) {   // a masked token does not count, even one that is not finite
+                                if (s[u][nt][2 * w] == -INFINITY) x0 = y0 = 0.f;
+                                if (s[u][nt][2 * w + 1] == -INFINITY) x1 = y1 = 0.f;
+                            }
+                            om[nt][ng][0] += y0;
+                            om[nt][ng][1] += y1;
+                            pb[nt][ng][w] = mov_trans(pack_h2(x0, x1));
+                        }
                 }
+                // O^T += V^T P^T: a thread's tokens are those of operand columns 2 t4, 2 t4 + 1 and 8 above.
+                const int ta = 2 * t4 + (t4 & 1), tb = 2 * t4 + 1 - (t4 & 1);
 #pragma unroll
-                for (int ng = 0; ng < NG; ++ng)
+                for (int ng = 0; ng < NG; ++ng) {
+                    const unsigned char *v = st + u * GB + HB + 32 * ng + 4 * g;
+                    uint32_t lo[2][4], hi[2][4];
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
-                        const float vr = vs[ng][w] * rs;
-                        float x0 = p[2 * w] * vr, x1 = p[2 * w + 1] * vr;
-                        float y0 = p[2 * w] * vl[ng][w], y1 = p[2 * w + 1] * vl[ng][w];
-                        if (edge) {   // a masked token does not count, even one that is not finite
-                            if (s[nt][2 * w] == -INFINITY) x0 = y0 = 0.f;
-                            if (s[nt][2 * w + 1] == -INFINITY) x1 = y1 = 0.f;
-                        }
-                        om[nt][ng][0] += y0;
-                        om[nt][ng][1] += y1;
-                        pb[nt][ng][w] = mov_trans(pack_h2(x0, x1));
+                        const uint32_t x = *reinterpret_cast<const uint32_t *>(v + (ta + 8 * w) * (DIM / 2));
+                        const uint32_t y = *reinterpret_cast<const uint32_t *>(v + (tb + 8 * w) * (DIM / 2));
+                        unpack_h(__byte_perm(x, y, 0x5410), lo[w], kc);   // dimensions 8 g + 0 .. 3 of both tokens
+                        unpack_h(__byte_perm(x, y, 0x7632), hi[w], kc);   // 8 g + 4 .. 7
                     }
-            }
-            // O^T += V^T P^T: a thread's tokens are those of operand columns 2 t4, 2 t4 + 1 and 8 above.
-            const int ta = 2 * t4 + (t4 & 1), tb = 2 * t4 + 1 - (t4 & 1);
 #pragma unroll
-            for (int ng = 0; ng < NG; ++ng) {
-                const unsigned char *v = st + HB + 32 * ng + 4 * g;
-                uint32_t lo[2][4], hi[2][4];
+                    for (int mt = 0; mt < 4; ++mt) {
+                        const uint32_t(&z)[2][4] = mt < 2 ? lo : hi;
+                        const int i = 2 * (mt & 1);
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const uint32_t x = *reinterpret_cast<const uint32_t *>(v + (ta + 8 * w) * (DIM / 2));
-                    const uint32_t y = *reinterpret_cast<const uint32_t *>(v + (tb + 8 * w) * (DIM / 2));
-                    unpack_h(__byte_perm(x, y, 0x5410), lo[w], kc);   // dimensions 8 g + 0 .. 3 of both tokens
-                    unpack_h(__byte_perm(x, y, 0x7632), hi[w], kc);   // 8 g + 4 .. 7
-                }
-#pragma unroll
-                for (int mt = 0; mt < 4; ++mt) {
-                    const uint32_t(&z)[2][4] = mt < 2 ? lo : hi;
-                    const int i = 2 * (mt & 1);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma<false>(o[nt][ng][mt], z[0][i], z[0][i + 1], z[1][i], z[1][i + 1], pb[nt][ng][0], pb[nt][ng][1]);
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma<false>(o[nt][ng][mt], z[0][i], z[0][i + 1], z[1][i], z[1][i + 1], pb[nt][ng][0], pb[nt][ng][1]);
+                    }
                 }
             }
+        };
+
+        const int gend = comp.g1();
+        for (int gi = comp.g0() + U * warp; gi < gend; gi += ROUND) {
+            cp_wait<kStages - 2>();
+            __syncwarp();
+            issue();
+            const uint32_t bits = (valid >> (out_slot * U)) & ((1u << U) - 1);
+            const unsigned char *st = sm.ring[warp][out_slot];
+            out_slot = out_slot + 1 == kStages ? 0 : out_slot + 1;
+            if (bits == (1u << U) - 1 && (gi + U) * LORA_KV_GRANULE - 1 <= least) step(std::false_type{}, st, gi, bits);
+            else if (bits) step(std::true_type{}, st, gi, bits);
         }
 
         // Join the warps.
@@ -716,6 +763,8 @@ __global__ void __launch_bounds__(kThreads * kJoinGroups) kv_join_kernel(AttendA
 }
 
 int tiles_of(int hq, int hkv, int max_q) { return (long long)max_q * (hq / hkv) <= 8 ? 1 : 2; }
+template <int NT>
+constexpr int granules_at_once() { return NT == 1 ? 2 : 1; }
 
 constexpr size_t kSplitBytes = (kMaxCtas * sizeof(Split) + 255) / 256 * 256;
 
@@ -723,11 +772,12 @@ template <int DIM, int NT, bool BF>
 int launch(const AttendArgs &a, cudaStream_t st) {
     Split *split = static_cast<Split *>(a.ws);
     float *part = reinterpret_cast<float *>(static_cast<char *>(a.ws) + kSplitBytes);
-    const size_t smem = sizeof(Smem<DIM, NT>);
-    if (int rc = cuda_check(cudaFuncSetAttribute(kv_attend_kernel<DIM, NT, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
+    constexpr int U = granules_at_once<NT>();
+    const size_t smem = sizeof(Smem<DIM, NT, U>);
+    if (int rc = cuda_check(cudaFuncSetAttribute(kv_attend_kernel<DIM, NT, U, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
         return rc;
-    const int grid = NT == 1 ? kMaxCtas : kMaxCtas / 4 * 3;
-    kv_attend_kernel<DIM, NT, BF><<<grid, kThreads, smem, st>>>(a, split, part);
+    const int grid = kMaxCtas;
+    kv_attend_kernel<DIM, NT, U, BF><<<grid, kThreads, smem, st>>>(a, split, part);
     count_launch();
     if (int rc = cuda_check(cudaGetLastError())) return rc;
     cudaLaunchConfig_t cfg{};
