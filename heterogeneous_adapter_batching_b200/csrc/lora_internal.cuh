@@ -88,6 +88,9 @@ namespace lora {
 bool tma_supported();
 int make_tensor_map(CUtensorMap *m, CUtensorMapDataType dt, int esize, const void *base, uint64_t cols,
                     uint64_t rows, uint32_t box_cols, uint32_t box_rows, bool swizzle128);
+// A tensor [d2][d1][d0] with byte strides for its outer two dimensions, boxes box2 x box1 x box0, 128-byte swizzle.
+int make_tensor_map_3d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t d0, uint64_t d1, uint64_t d2,
+                       uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2);
 // The pool's map: a box is 64 columns x 16 rows (one page high), 128-byte swizzle.
 int pool_tensor_map(lora_pool_s *pool, CUtensorMap *out);
 // The pool seen in 3D, (column, row, 64-column step): one box (64, 16, 4) lands

@@ -19,6 +19,13 @@ bool rows_ok(const lora_rows_t *r, int heads, int dtype) {
     return r->token_stride % e == 0 && r->head_stride % e == 0;
 }
 
+// Strides that a TMA descriptor takes: positive where they count, below 2^40 bytes (of 16-bit elements).
+bool strides_ok(const lora_rows_t *r, int T, int heads) {
+    if (T < 1) return true;
+    return (T == 1 || (r->token_stride > 0 && r->token_stride < (1LL << 39))) &&
+           (heads == 1 || (r->head_stride > 0 && r->head_stride < (1LL << 39)));
+}
+
 Rows rows(const lora_rows_t *r) { return r ? Rows{r->data, r->token_stride, r->head_stride} : Rows{nullptr, 0, 0}; }
 
 int check_cache(const lora_kv_cache_t *c) {
@@ -167,6 +174,7 @@ int lora_prompt_attend(const lora_rows_t *q, const lora_rows_t *k, const lora_ro
     if (!rows_ok(q, q_heads, dtype) || !rows_ok(out, q_heads, dtype) || !rows_ok(k, Tk ? kv_heads : 0, dtype) ||
         !rows_ok(v, Tk ? kv_heads : 0, dtype))
         return LORA_ERR_INVALID_ARG;
+    if (!strides_ok(q, Tq, q_heads) || !strides_ok(k, Tk, kv_heads) || !strides_ok(v, Tk, kv_heads)) return LORA_ERR_INVALID_ARG;
     const PromptArgs a{rows(q), rows(k), rows(v), rows(out), Tq, Tk, q_heads, kv_heads, head_dim, dtype,
                        cu_q, cu_k, R, scale, lse, err_dev};
     return launch_prompt(a, reinterpret_cast<cudaStream_t>(stream));

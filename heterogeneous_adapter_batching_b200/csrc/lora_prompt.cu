@@ -1,100 +1,470 @@
-// Attention, plain: one CTA per (query row, query head), its warps stride over
-// the keys with a running maximum and sum each, and are joined at the end.
+// Causal attention over packed prompts on the 5th-generation tensor cores.
+//
+// out = sum_j p_j v_j / sum_j p_j, p_j = exp(scale q . k_j), j <= m - n + i for
+// query i of a request with n query and m key rows.  A CTA owns two tiles of
+// 128 query rows of one kv head and walks the keys in tiles of 128 with a
+// running reference for the exponent, the scores and the output accumulators in
+// tensor memory:
+//   S_t = Q_t K^T     tcgen05.mma, both operands in shared memory (TMA, SW128)
+//   P_t = exp2(S_t)   one thread per row reads S_t from tensor memory and writes
+//                     P_t, rounded to the row type, over it
+//   O_t += P_t V      tcgen05.mma, A = P_t in tensor memory, B = V as TMA lays it
+//                     (keys x dims, read MN-major)
+// While one tile's scores go through the exponential the tensor cores work on the
+// other.  Per 128 x 128 tile at head_dim 128 the two products take 1024 cycles and
+// the 16384 exponentials 1024 cycles of the 16-wide unit, so the two are balanced
+// and everything else has to hide behind them.
+//
+// Rows of a tile are tokens x PK query heads of the kv head (PK: the largest
+// power of two that divides the group), token major: a short prompt fills
+// more of a tile, and a group shares its keys' and values' way through shared
+// memory.
+//
+// The reference of a row moves only when a score exceeds it by 8 powers of two;
+// O_t is then rescaled in tensor memory by the row's own thread.  S_t of the next
+// keys is issued behind the product that reads P_t, so its arrival also says that
+// O_t is at rest.
+//
+// Roles: warp 0 loads, warp 1 issues the products (one lane) and clears the values
+// behind a request's last key in its last tile, warps 4-7 and 8-11 own tile 0 and
+// 1.  Waits are bounded (LORA_DEV_ERR_TIMEOUT).  No cluster multicast.
+#include <cuda.h>
+
+#include <type_traits>
+
 #include "lora_internal.cuh"
 #include "lora_kv.cuh"
+#include "lora_ptx.cuh"
 
 namespace lora {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kThreads = 384;
+constexpr int kM = 128, kN = 128;    // rows of a tile, keys of a tile
+constexpr float kJump = 8.f;         // log2 by which a score may exceed the reference
+constexpr long long kWaitLimit = 2000000000LL;
 
-template <class H>
-__device__ __forceinline__ float to_f(H x) { return (float)x; }
+template <int DIM>
+constexpr int stages() { return DIM == 128 ? 5 : 8; }
 
-template <int DIM, class H>
-struct DenseKv {
-    const H *kp, *vp;
-    long long kts, vts;
-    __device__ __forceinline__ bool at(int j, float (&k)[DIM / 32], float (&v)[DIM / 32]) const {
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int i = 0; i < DIM / 32; ++i) {
-            k[i] = (float)kp[j * kts + lane * (DIM / 32) + i];
-            v[i] = (float)vp[j * vts + lane * (DIM / 32) + i];
-        }
-        return true;
-    }
+template <int DIM>
+struct Smem {
+    unsigned char q[2][kM * DIM * 2];              // [dim half][row][64] SW128
+    unsigned char kv[stages<DIM>()][kN * DIM * 2]; // the same
+    uint64_t q_full, full[stages<DIM>()], empty[stages<DIM>()], s_full[2], p_ready[2], o_full[2], drain;
+    uint32_t tmem;
+    int abort;
+    int item[2];   // request and its tile pair
 };
 
-template <int DIM, class H, class Kv>
-__device__ __forceinline__ void attend_row(const Kv &kv, int n, const H *q, H *o, float *lse, float scale) {
-    constexpr int E = DIM / 32;
-    __shared__ float sm_m[kWarps], sm_l[kWarps], sm_o[kWarps][DIM];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float qv[E], acc[E] = {}, m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) qv[i] = to_f(q[lane * E + i]) * scale;
-    for (int j = warp; j < n; j += kWarps) {
-        float k[E], v[E], s = 0.f;
-        if (!kv.at(j, k, v)) continue;
-#pragma unroll
-        for (int i = 0; i < E; ++i) s = fmaf(qv[i], k[i], s);
-        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-        const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn, f = __expf(m - ref), p = __expf(s - ref);
-        l = l * f + p;
-#pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = acc[i] * f + (p > 0.f || p != p ? p * v[i] : 0.f);
-        m = mn;
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+struct KArgs {
+    void *o;
+    long long ots, ohs;
+    float *lse;
+    const int32_t *cu_q, *cu_k;
+    int Tq, Tk, R, hq, G, pk, groups;   // pk: heads in a tile; groups: tiles' head blocks, hq / pk
+    float scale;
+    int32_t *err;
+};
+
+template <class Sm>
+__device__ __forceinline__ bool wait(uint64_t *b, uint32_t parity, Sm &sm, int32_t *err) {
+    const uint32_t a = ptx::smem_u32(b);
+    if (ptx::mbar_try(a, parity)) return true;
+    const long long t0 = clock64();
+    while (!ptx::mbar_try(a, parity)) {
+        if (*(volatile int *)&sm.abort) return false;
+        if (clock64() - t0 > kWaitLimit) {
+            *(volatile int *)&sm.abort = 1;
+            if (err) atomicOr(err, LORA_DEV_ERR_TIMEOUT);
+            return false;
+        }
     }
-    if (lane == 0) {
-        sm_m[warp] = m;
-        sm_l[warp] = l;
+    return true;
+}
+// For this thread's own asynchronous work before the CTA exits: bounded, not cut short by the abort flag.
+__device__ __forceinline__ void drain_wait(uint64_t *b, uint32_t parity) {
+    const long long t0 = clock64();
+    while (!ptx::mbar_try(ptx::smem_u32(b), parity) && clock64() - t0 < kWaitLimit / 8) {
     }
-#pragma unroll
-    for (int i = 0; i < E; ++i) sm_o[warp][lane * E + i] = acc[i];
-    __syncthreads();
-    float mm = -INFINITY, ll = 0.f;
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w]);
-    const float ref = mm == -INFINITY ? 0.f : mm;   // scores may all be NaN
-    for (int w = 0; w < kWarps; ++w) ll += sm_l[w] * __expf(sm_m[w] - ref);
-    for (int d = threadIdx.x; d < DIM; d += kWarps * 32) {
-        float s = 0.f;
-        for (int w = 0; w < kWarps; ++w) s += sm_o[w][d] * __expf(sm_m[w] - ref);
-        o[d] = (H)(ll == 0.f ? 0.f : s / ll);
-    }
-    if (lse && threadIdx.x == 0) *lse = ref + logf(ll);
 }
 
-template <int DIM, class H>
-__global__ void __launch_bounds__(kWarps * 32) attend_prompt_kernel(PromptArgs a) {
-    const int t = blockIdx.x, hq = blockIdx.y, h = hq / (a.hq / a.hkv);
-    for (int r = 0; r < a.R; ++r) {
-        const int q0 = a.cu_q[r], q1 = a.cu_q[r + 1], k0 = a.cu_k[r], k1 = a.cu_k[r + 1];
-        if (q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk) {
-            if (a.err && threadIdx.x == 0 && t == 0 && hq == 0) atomicOr(a.err, LORA_DEV_ERR_BAD_LENGTH);
-            continue;
+__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 | (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// kind::f16 with fp32 accumulators; type 0 = fp16, 1 = bf16.
+constexpr uint32_t idesc(int type, int N, int b_mn) {
+    return 1u << 4 | (uint32_t)type << 7 | (uint32_t)type << 10 | (uint32_t)b_mn << 16 | (uint32_t)(N >> 3) << 17 | (uint32_t)(kM >> 4) << 24;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define R8(r, i) "=f"(r[i]), "=f"(r[i + 1]), "=f"(r[i + 2]), "=f"(r[i + 3]), "=f"(r[i + 4]), "=f"(r[i + 5]), "=f"(r[i + 6]), "=f"(r[i + 7])
+#define W8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+__device__ __forceinline__ void ld32(float (&r)[32], uint32_t addr) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+                 "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];" : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24) : "r"(addr));
+}
+__device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 ::"r"(addr), W8(r, 0), W8(r, 8) : "memory");
+}
+__device__ __forceinline__ void st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+                 "%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr), W8(r, 0), W8(r, 8), W8(r, 16), W8(r, 24) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t y;
+    if (BF) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+
+// Tile pairs of request r (0 past the last), -1 if its row ranges are none.
+__device__ __forceinline__ int pairs_of(const KArgs &a, int r, int toks) {
+    if (r >= a.R) return 0;
+    const int q0 = a.cu_q[r], q1 = a.cu_q[r + 1], k0 = a.cu_k[r], k1 = a.cu_k[r + 1];
+    if (q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk) return -1;
+    return (q1 - q0 + 2 * toks - 1) / (2 * toks);
+}
+
+template <int DIM, bool BF>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Maps maps, KArgs a) {
+    using H = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+    constexpr int ST = stages<DIM>(), HALVES = DIM / 64;
+    constexpr uint32_t TILE = kN * DIM * 2, HALF = kN * 128;   // bytes of a tile and of its 64-column block
+    constexpr float kShift = BF ? 0.f : 7.f;                   // fp16 weights are scaled by 2^7: room below for small ones
+    extern __shared__ unsigned char raw[];
+    Smem<DIM> &sm = *reinterpret_cast<Smem<DIM> *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int hb = blockIdx.x % a.groups, want = blockIdx.x / a.groups, toks = kM / a.pk;   // tokens of a tile
+
+    if (warp == 0) {
+        // The item's request: tile pairs are numbered request by request.
+        int base = 0, found = -1, pair = 0;
+        for (int r0 = 0; r0 < a.R && found < 0; r0 += 32) {
+            const int n = max(0, pairs_of(a, r0 + lane, toks));
+            int run = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int x = __shfl_up_sync(~0u, run, d);
+                if (lane >= d) run += x;
+            }
+            const uint32_t hit = __ballot_sync(~0u, base + run > want);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                found = r0 + l;
+                pair = base + __shfl_sync(~0u, run, l) - 1 - want;   // the longest rows of a request first
+            }
+            base += __shfl_sync(~0u, run, 31);
         }
-        if (t < q0 || t >= q1) continue;
-        __syncthreads();
-        const DenseKv<DIM, H> kv{reinterpret_cast<const H *>(a.k.p) + k0 * a.k.ts + h * a.k.hs,
-                                 reinterpret_cast<const H *>(a.v.p) + k0 * a.v.ts + h * a.v.hs, a.k.ts, a.v.ts};
-        attend_row<DIM, H>(kv, (k1 - k0) - (q1 - q0) + (t - q0) + 1,
-                           reinterpret_cast<const H *>(a.q.p) + t * a.q.ts + hq * a.q.hs,
-                           reinterpret_cast<H *>(a.o.p) + t * a.o.ts + hq * a.o.hs,
-                           a.lse ? a.lse + (size_t)t * a.hq + hq : nullptr, a.scale);
+        if (blockIdx.x == 0)
+            for (int r = lane; r < a.R; r += 32)
+                if (pairs_of(a, r, toks) < 0 && a.err) atomicOr(a.err, LORA_DEV_ERR_BAD_LENGTH);
+        if (lane == 0) {
+            sm.item[0] = found;
+            sm.item[1] = pair;
+        }
     }
+    if (tid == 0) {
+        ptx::mbar_init(&sm.q_full, 1);
+        for (int s = 0; s < ST; ++s) {
+            ptx::mbar_init(&sm.full[s], 1);
+            ptx::mbar_init(&sm.empty[s], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(&sm.s_full[t], 1);
+            ptx::mbar_init(&sm.p_ready[t], 4);
+            ptx::mbar_init(&sm.o_full[t], 1);
+        }
+        ptx::mbar_init(&sm.drain, 1);
+        sm.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    const int r = sm.item[0];
+    if (r < 0) return;
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(ptx::smem_u32(&sm.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = sm.tmem;
+
+    const int q0 = a.cu_q[r], nq = a.cu_q[r + 1] - q0, k0 = a.cu_k[r], nk = a.cu_k[r + 1] - k0;
+    const int tok0 = sm.item[1] * 2 * toks, back = nk - nq;          // first token of tile 0; query i sees keys <= back + i
+    // key tiles of each query tile: up to the last key its last token sees
+    int nt[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int first = tok0 + t * toks, last = min(nq, first + toks) - 1;
+        nt[t] = last < first || back + last < 0 ? 0 : (back + last) / kN + 1;
+    }
+    const int total = max(nt[0], nt[1]);
+    const int tail_rows = nk - (total - 1) * kN;                     // rows of the last key tile that are the request's (maybe more than kN)
+    const int head = hb * a.pk, kvh = head / a.G;
+
+    if (warp == 0) {
+        if (lane == 0 && total > 0) {
+            ptx::mbar_expect_tx(&sm.q_full, 2 * TILE);
+            for (int t = 0; t < 2; ++t)
+                for (int h = 0; h < HALVES; ++h)
+                    ptx::tma_load_3d(sm.q[t] + h * HALF, &maps.q, h * 64, head, q0 + tok0 + t * toks, &sm.q_full);
+            int i = 0;
+            for (; i < 2 * total; ++i) {
+                const int s = i % ST;
+                if (i >= ST && !wait(&sm.empty[s], (i / ST - 1) & 1, sm, a.err)) break;
+                ptx::mbar_expect_tx(&sm.full[s], TILE);
+                for (int h = 0; h < HALVES; ++h)
+                    ptx::tma_load_3d(sm.kv[s] + h * HALF, (i & 1) ? &maps.v : &maps.k, h * 64, kvh, k0 + (i >> 1) * kN, &sm.full[s]);
+            }
+            if (*(volatile int *)&sm.abort) {   // loads in flight land before the CTA goes
+                drain_wait(&sm.q_full, 0);
+                for (int j = max(0, i - ST); j < i; ++j) drain_wait(&sm.full[j % ST], (j / ST) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (total > 0) {
+            constexpr uint32_t id_s = idesc(BF ? 1 : 0, kN, 0), id_o = idesc(BF ? 1 : 0, DIM, 1);
+            const auto scores = [&](int t, int s) {   // one lane
+                const uint64_t dq = sdesc(ptx::smem_u32(sm.q[t]), 16, 1024), dk = sdesc(ptx::smem_u32(sm.kv[s]), 16, 1024);
+#pragma unroll
+                for (int k = 0; k < DIM / 16; ++k) {
+                    const uint64_t off = (k / 4) * (HALF >> 4) + (k % 4) * 2;
+                    mma_ss(tmem + t * kN, dq + off, dk + off, id_s, k != 0);
+                }
+                commit(&sm.s_full[t]);
+            };
+            const auto await = [&](uint64_t *b, uint32_t parity) { return (bool)__all_sync(~0u, wait(b, parity, sm, a.err)); };
+            bool ok = await(&sm.q_full, 0) && await(&sm.full[0], 0);
+            if (ok && lane == 0) {
+                fence_after();
+                for (int t = 0; t < 2; ++t)
+                    if (nt[t] > 0) scores(t, 0);
+                commit(&sm.empty[0]);
+            }
+            for (int j = 0; ok && j < total; ++j) {
+                const int vs = (2 * j + 1) % ST, ks = (2 * j + 2) % ST;
+                ok = await(&sm.full[vs], ((2 * j + 1) / ST) & 1);
+                if (ok && j == total - 1 && tail_rows < kN) {
+                    // values behind the request's last key: other rows, whatever they hold; 0 x NaN would reach this request
+                    for (int x = tail_rows * 8 + lane; x < kN * 8; x += 32)
+                        for (int h = 0; h < HALVES; ++h)
+                            *reinterpret_cast<uint4 *>(sm.kv[vs] + h * HALF + x * 16) = make_uint4(0, 0, 0, 0);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                if (ok && j + 1 < total) ok = await(&sm.full[ks], ((2 * j + 2) / ST) & 1);
+                const uint64_t dv = sdesc(ptx::smem_u32(sm.kv[vs]), HALF, 1024);
+                for (int t = 0; ok && t < 2; ++t) {
+                    if (j >= nt[t]) continue;
+                    ok = await(&sm.p_ready[t], j & 1);
+                    if (ok && lane == 0) {
+                        fence_after();
+#pragma unroll
+                        for (int k = 0; k < kN / 16; ++k)
+                            mma_ts(tmem + 2 * kN + t * 128, tmem + t * kN + k * 8, dv + (uint64_t)(k * (2048 >> 4)), id_o, j != 0 || k != 0);
+                        if (j + 1 < nt[t]) scores(t, ks);
+                        else commit(&sm.o_full[t]);
+                    }
+                }
+                if (ok && lane == 0) {
+                    commit(&sm.empty[vs]);
+                    if (j + 1 < total) commit(&sm.empty[ks]);
+                }
+            }
+            if (lane == 0) {
+                commit(&sm.drain);
+                drain_wait(&sm.drain, 0);   // no product runs when the CTA goes
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int t = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // the warp's 32 lanes of tensor memory
+        const uint32_t ts = tmem + t * kN + lanes, to = tmem + 2 * kN + t * 128 + lanes;
+        const int tok = tok0 + t * toks + row / a.pk, hq = head + row % a.pk;
+        const bool mine = tok < nq;
+        const int lim = min(back + tok, nk - 1);                      // last key this row sees
+        const int least = min(back + tok0 + t * toks, nk - 1);        // of the tile's first row
+        const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f), jump = kJump / c;
+        const bool neg = a.scale < 0.f;
+        float m = -INFINITY, mc = -kShift, thr = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < nt[t]; ++j) {
+            ok = wait(&sm.s_full[t], j & 1, sm, a.err);
+            if (!__all_sync(~0u, ok)) break;
+            fence_after();
+            const bool edge = j * kN + kN - 1 > least;
+            const auto load = [&](float (&s)[32], int ch) {
+                ld32(s, ts + ch * 32);
+                wait_ld();
+                if (neg)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) s[e] = -s[e];
+                if (edge) {
+                    const int from = lim - j * kN - ch * 32;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (e > from) s[e] = -INFINITY;
+                }
+            };
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int ch = 0; ch < 4; ++ch) {
+                float s[32];
+                load(s, ch);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e]);
+            }
+            const bool up = top > thr;
+            if (__any_sync(~0u, up)) {
+                const float n = up ? top : m;
+                const float f = !up ? 1.f : m == -INFINITY ? 0.f : ex2((m - n) * c);
+                m = n;
+                mc = (n == -INFINITY ? 0.f : n * c) - kShift;
+                thr = n + jump;
+                l *= f;
+                if (j > 0) {
+#pragma unroll 1
+                    for (int ch = 0; ch < DIM / 32; ++ch) {
+                        float o[32];
+                        ld32(o, to + ch * 32);
+                        wait_ld();
+                        uint32_t u[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
+                        st32(to + ch * 32, u);
+                    }
+                }
+            }
+#pragma unroll 1
+            for (int ch = 0; ch < 4; ++ch) {
+                float s[32];
+                load(s, ch);
+                uint32_t p[16];
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float x = ex2(fmaf(s[2 * e], c, -mc)), y = ex2(fmaf(s[2 * e + 1], c, -mc));
+                    sum += x + y;
+                    p[e] = pack<BF>(x, y);
+                }
+                l += sum;
+                st16(ts + ch * 16, p);
+            }
+            wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sm.p_ready[t]);
+        }
+        ok = __all_sync(~0u, ok);
+        if (ok && nt[t] > 0) {
+            ok = wait(&sm.o_full[t], 0, sm, a.err);
+            ok = __all_sync(~0u, ok);
+            fence_after();
+        }
+        if (ok) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            H *out = reinterpret_cast<H *>(a.o) + (long long)(q0 + tok) * a.ots + (long long)hq * a.ohs;
+#pragma unroll 1
+            for (int ch = 0; ch < DIM / 32; ++ch) {
+                float o[32];
+                if (nt[t] > 0) {
+                    ld32(o, to + ch * 32);
+                    wait_ld();
+                }
+                if (mine) {
+                    const bool none = l == 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint4 u = make_uint4(0, 0, 0, 0);
+                        if (!none) {
+                            u.x = pack<BF>(o[8 * i] * inv, o[8 * i + 1] * inv);
+                            u.y = pack<BF>(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
+                            u.z = pack<BF>(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
+                            u.w = pack<BF>(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
+                        }
+                        *reinterpret_cast<uint4 *>(out + ch * 32 + 8 * i) = u;
+                    }
+                }
+            }
+            if (a.lse && mine) a.lse[(size_t)(q0 + tok) * a.hq + hq] = l == 0.f ? -INFINITY : 0.6931471805599453f * (mc + log2f(l));
+        }
+    }
+
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// [tokens][heads][dim] rows as a 3D map with boxes of 64 dims x `heads` x `toks`, 128-byte swizzle.
+int rows_map(CUtensorMap *m, const Rows &r, int dim, int heads, int T, int dtype, int box_heads, int box_toks) {
+    // the stride of a dimension with one element is free
+    const uint64_t ts = T > 1 ? (uint64_t)r.ts * 2 : 16, hs = heads > 1 ? (uint64_t)r.hs * 2 : 16;
+    return make_tensor_map_3d(m, dtype == LORA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, r.p,
+                              (uint64_t)dim, (uint64_t)heads, (uint64_t)(T > 0 ? T : 1), hs, ts, 64, box_heads, box_toks);
+}
+
+template <int DIM, bool BF>
+int launch(const PromptArgs &a, cudaStream_t st) {
+    KArgs k{};
+    k.o = a.o.p; k.ots = a.o.ts; k.ohs = a.o.hs; k.lse = a.lse;
+    k.cu_q = a.cu_q; k.cu_k = a.cu_k; k.Tq = a.Tq; k.Tk = a.Tk; k.R = a.R;
+    k.hq = a.hq; k.G = a.hq / a.hkv; k.scale = a.scale; k.err = a.err;
+    k.pk = k.G & -k.G;
+    k.groups = a.hq / k.pk;
+    const int pair = 2 * kM / k.pk;                                     // tokens of a CTA
+    const long long items = ((long long)a.Tq / pair + a.R) * k.groups;  // at least the tile pairs of any row ranges
+    if (items > INT32_MAX) return LORA_ERR_TOO_LARGE;
+    Maps maps;
+    // without keys nothing is loaded: any valid address serves
+    const Rows kr = a.Tk > 0 ? a.k : a.q, vr = a.Tk > 0 ? a.v : a.q;
+    if (int rc = rows_map(&maps.q, a.q, DIM, a.hq, a.Tq, a.dtype, k.pk, kM / k.pk)) return rc;
+    if (int rc = rows_map(&maps.k, kr, DIM, a.hkv, a.Tk, a.dtype, 1, kN)) return rc;
+    if (int rc = rows_map(&maps.v, vr, DIM, a.hkv, a.Tk, a.dtype, 1, kN)) return rc;
+    const size_t smem = sizeof(Smem<DIM>) + 1024;
+    static_assert(sizeof(Smem<DIM>) + 1024 <= 227 * 1024, "prompt kernel: shared memory beyond the per-block limit");
+    if (int rc = cuda_check(cudaFuncSetAttribute(prompt_kernel<DIM, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))) return rc;
+    prompt_kernel<DIM, BF><<<(int)items, kThreads, smem, st>>>(maps, k);
+    count_launch();
+    return cuda_check(cudaGetLastError());
 }
 
 }  // namespace
 
 int launch_prompt(const PromptArgs &a, cudaStream_t st) {
-    const dim3 grid(a.Tq, a.hq);
-    if (a.dim == 64 && a.dtype == LORA_BF16) attend_prompt_kernel<64, __nv_bfloat16><<<grid, kWarps * 32, 0, st>>>(a);
-    else if (a.dim == 64) attend_prompt_kernel<64, __half><<<grid, kWarps * 32, 0, st>>>(a);
-    else if (a.dtype == LORA_BF16) attend_prompt_kernel<128, __nv_bfloat16><<<grid, kWarps * 32, 0, st>>>(a);
-    else attend_prompt_kernel<128, __half><<<grid, kWarps * 32, 0, st>>>(a);
-    count_launch();
-    return cuda_check(cudaGetLastError());
+    if (!tma_supported()) return LORA_ERR_CUDA;
+    if (a.dim == 64) return a.dtype == LORA_BF16 ? launch<64, true>(a, st) : launch<64, false>(a, st);
+    return a.dtype == LORA_BF16 ? launch<128, true>(a, st) : launch<128, false>(a, st);
 }
 
 }  // namespace lora

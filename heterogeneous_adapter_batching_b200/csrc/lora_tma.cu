@@ -45,6 +45,19 @@ int make_tensor_map(CUtensorMap *m, CUtensorMapDataType dt, int esize, const voi
     return r == CUDA_SUCCESS ? LORA_OK : LORA_ERR_CUDA;
 }
 
+int make_tensor_map_3d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t d0, uint64_t d1, uint64_t d2,
+                       uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return LORA_ERR_CUDA;
+    cuuint64_t dims[3] = {d0, d1, d2};
+    cuuint64_t strides[2] = {stride1, stride2};
+    cuuint32_t box[3] = {box0, box1, box2};
+    cuuint32_t es[3] = {1, 1, 1};
+    CUresult r = enc(m, dt, 3, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? LORA_OK : LORA_ERR_CUDA;
+}
+
 int pool_tensor_map(lora_pool_s *pool, CUtensorMap *out) {
     if (!pool) return LORA_ERR_INVALID_ARG;
     std::lock_guard<std::mutex> g(pool->mu);

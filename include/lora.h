@@ -561,7 +561,9 @@ int lora_kv_attend(const lora_rows_t *q, int T, int q_heads, int dtype, const lo
  * lora_kv_attend.  n = m for whole prompts (cu_k may be cu_q); m > n when a
  * prefix comes from the cache (lora_kv_gather).
  *   q, out [Tq][q_heads], k, v [Tk][kv_heads] rows of dtype (LORA_BF16 or
- *   LORA_FP16), head_dim 64 or 128; lse [Tq][q_heads] fp32 or NULL.  cu_q, cu_k
+ *   LORA_FP16), head_dim 64 or 128; strides of q, k and v are positive (where
+ *   there is more than one token or head) and below 2^40 bytes; lse
+ *   [Tq][q_heads] fp32 or NULL.  cu_q, cu_k
  *   [R+1] int32 on the device, not decreasing, within [0, Tq] and [0, Tk]: a
  *   request that is not sets LORA_DEV_ERR_BAD_LENGTH and its rows are left alone.
  * Rows outside [cu_q[0], cu_q[R]) are left alone.  A row that attends to nothing
