@@ -136,6 +136,20 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 template <bool BF>
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t y;
@@ -323,26 +337,31 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             if (!__all_sync(~0u, ok)) break;
             fence_after();
             const bool edge = j * kN + kN - 1 > least;
-            const auto load = [&](float (&s)[32], int ch) {
-                ld32(s, ts + ch * 32);
-                wait_ld();
-                if (neg)
+            float x[4][32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) s[e] = -s[e];
-                if (edge) {
-                    const int from = lim - j * kN - ch * 32;
+            for (int ch = 0; ch < 4; ++ch) ld32(x[ch], ts + ch * 32);
+            wait_ld();
+            if (neg) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (e > from) s[e] = -INFINITY;
-                }
-            };
+                for (int e = 0; e < kN; ++e) x[e / 32][e % 32] = -x[e / 32][e % 32];
+            }
+            if (edge) {
+                const int from = lim - j * kN;
+#pragma unroll
+                for (int e = 0; e < kN; ++e)
+                    if (e > from) x[e / 32][e % 32] = -INFINITY;
+            }
             float top = -INFINITY;
-#pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
-                float s[32];
-                load(s, ch);
+            {
+                float u[4];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e]);
+                for (int ch = 0; ch < 4; ++ch) {
+                    u[ch] = x[ch][0];
+#pragma unroll
+                    for (int e = 1; e < 31; e += 2) u[ch] = fmaxf(u[ch], fmaxf(x[ch][e], x[ch][e + 1]));
+                    u[ch] = fmaxf(u[ch], x[ch][31]);
+                }
+                top = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3]));
             }
             const bool up = top > thr;
             if (__any_sync(~0u, up)) {
@@ -365,21 +384,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     }
                 }
             }
-#pragma unroll 1
+            const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+            float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
             for (int ch = 0; ch < 4; ++ch) {
-                float s[32];
-                load(s, ch);
                 uint32_t p[16];
-                float sum = 0.f;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float x = ex2(fmaf(s[2 * e], c, -mc)), y = ex2(fmaf(s[2 * e + 1], c, -mc));
-                    sum += x + y;
-                    p[e] = pack<BF>(x, y);
+                    const float2 y = fma2(make_float2(x[ch][2 * e], x[ch][2 * e + 1]), c2, mc2);
+                    const float2 w = make_float2(ex2(y.x), ex2(y.y));
+                    sum[e & 1] = add2(sum[e & 1], w);
+                    p[e] = pack<BF>(w.x, w.y);
                 }
-                l += sum;
                 st16(ts + ch * 16, p);
             }
+            l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             wait_st();
             fence_before();
             __syncwarp();
