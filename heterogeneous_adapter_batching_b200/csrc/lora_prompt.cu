@@ -25,9 +25,17 @@
 // keys is issued behind the product that reads P_t, so its arrival also says that
 // O_t is at rest.
 //
+// One CTA per SM works through a list of items (request, tile pair, head block)
+// without draining its pipelines between them: the next item's queries are loaded
+// when the current one's last scores are done, its keys follow the current one's
+// values through the same ring, and its first scores are issued while the row
+// owners still write the current outputs.  Items are taken in the order of 16
+// classes of work, most keys first, so that the last ones are small.
+//
 // Roles: warp 0 loads, warp 1 issues the products (one lane) and clears the values
-// behind a request's last key in its last tile, warps 4-7 and 8-11 own tile 0 and
-// 1.  Waits are bounded (LORA_DEV_ERR_TIMEOUT).  No cluster multicast.
+// behind a request's last key in its last tile, warp 3 lists the items, warps 4-7
+// and 8-11 own tile 0 and 1.  Waits are bounded (LORA_DEV_ERR_TIMEOUT).  No
+// cluster multicast.
 #include <cuda.h>
 
 #include <type_traits>
@@ -47,14 +55,22 @@ constexpr long long kWaitLimit = 2000000000LL;
 template <int DIM>
 constexpr int stages() { return DIM == 128 ? 5 : 8; }
 
+constexpr int kClasses = 16;
+
+struct Item {
+    int q0, nq, k0, nk, tok0, head;   // nq < 0: no more items
+};
+
 template <int DIM>
 struct Smem {
     unsigned char q[2][kM * DIM * 2];              // [dim half][row][64] SW128
     unsigned char kv[stages<DIM>()][kN * DIM * 2]; // the same
-    uint64_t q_full, full[stages<DIM>()], empty[stages<DIM>()], s_full[2], p_ready[2], o_full[2], drain;
+    uint64_t q_full[2], q_empty[2], full[stages<DIM>()], empty[stages<DIM>()], s_full[2], p_ready[2], o_full[2], drain;
+    uint64_t item_full[2], item_empty[2];
+    Item item[2];
     uint32_t tmem;
     int abort;
-    int item[2];   // request and its tile pair
+    int most, hist[kClasses];                      // most key tiles of an item; tile pairs of each class
 };
 
 struct Maps {
@@ -123,13 +139,13 @@ __device__ __forceinline__ void ld32(float (&r)[32], uint32_t addr) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
                  "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];" : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24) : "r"(addr));
 }
+__device__ __forceinline__ void ld16(float (&r)[16], uint32_t addr) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : R8(r, 0), R8(r, 8) : "r"(addr));
+}
 __device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
                  ::"r"(addr), W8(r, 0), W8(r, 8) : "memory");
-}
-__device__ __forceinline__ void st32(uint32_t addr, const uint32_t (&r)[32]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
-                 "%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr), W8(r, 0), W8(r, 8), W8(r, 16), W8(r, 24) : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -158,12 +174,27 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     return y;
 }
 
-// Tile pairs of request r (0 past the last), -1 if its row ranges are none.
-__device__ __forceinline__ int pairs_of(const KArgs &a, int r, int toks) {
-    if (r >= a.R) return 0;
+// A request's rows and keys; nq = -1 if its ranges are none.
+struct Req {
+    int q0, nq, k0, nk;
+};
+__device__ __forceinline__ Req request(const KArgs &a, int r) {
     const int q0 = a.cu_q[r], q1 = a.cu_q[r + 1], k0 = a.cu_k[r], k1 = a.cu_k[r + 1];
-    if (q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk) return -1;
-    return (q1 - q0 + 2 * toks - 1) / (2 * toks);
+    const bool bad = q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk;
+    return bad ? Req{0, -1, 0, 0} : Req{q0, q1 - q0, k0, k1 - k0};
+}
+// Key tiles that rows up to token `last` see.
+__device__ __forceinline__ int tiles_to(const Req &q, int last) {
+    const int key = q.nk - q.nq + last;
+    return key < 0 ? 0 : key / kN + 1;
+}
+// First tile pair (of 1 << sh tokens) of a request with at least x key tiles; its number of pairs if none.
+__device__ __forceinline__ int first_pair(const Req &q, int x, int sh) {
+    if (q.nq <= 0) return 0;
+    const int n = (q.nq - 1 >> sh) + 1;
+    if (x <= 0) return 0;
+    const long long last = (long long)(x - 1) * kN - (q.nk - q.nq);   // the first token that sees that many
+    return last <= 0 ? 0 : last > q.nq - 1 ? n : (int)(last >> sh);
 }
 
 template <int DIM, bool BF>
@@ -175,53 +206,28 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     extern __shared__ unsigned char raw[];
     Smem<DIM> &sm = *reinterpret_cast<Smem<DIM> *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int hb = blockIdx.x % a.groups, want = blockIdx.x / a.groups, toks = kM / a.pk;   // tokens of a tile
+    const int toks = kM / a.pk, sh = __ffs(toks);              // tokens of a tile; log2 of those of a pair
 
-    if (warp == 0) {
-        // The item's request: tile pairs are numbered request by request.
-        int base = 0, found = -1, pair = 0;
-        for (int r0 = 0; r0 < a.R && found < 0; r0 += 32) {
-            const int n = max(0, pairs_of(a, r0 + lane, toks));
-            int run = n;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int x = __shfl_up_sync(~0u, run, d);
-                if (lane >= d) run += x;
-            }
-            const uint32_t hit = __ballot_sync(~0u, base + run > want);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                found = r0 + l;
-                pair = base + __shfl_sync(~0u, run, l) - 1 - want;   // the longest rows of a request first
-            }
-            base += __shfl_sync(~0u, run, 31);
-        }
-        if (blockIdx.x == 0)
-            for (int r = lane; r < a.R; r += 32)
-                if (pairs_of(a, r, toks) < 0 && a.err) atomicOr(a.err, LORA_DEV_ERR_BAD_LENGTH);
-        if (lane == 0) {
-            sm.item[0] = found;
-            sm.item[1] = pair;
-        }
-    }
     if (tid == 0) {
-        ptx::mbar_init(&sm.q_full, 1);
         for (int s = 0; s < ST; ++s) {
             ptx::mbar_init(&sm.full[s], 1);
             ptx::mbar_init(&sm.empty[s], 1);
         }
         for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(&sm.q_full[t], 1);
+            ptx::mbar_init(&sm.q_empty[t], 1);
             ptx::mbar_init(&sm.s_full[t], 1);
             ptx::mbar_init(&sm.p_ready[t], 4);
             ptx::mbar_init(&sm.o_full[t], 1);
+            ptx::mbar_init(&sm.item_full[t], 1);
+            ptx::mbar_init(&sm.item_empty[t], 10);
         }
         ptx::mbar_init(&sm.drain, 1);
         sm.abort = 0;
+        sm.most = 0;
+        for (int b = 0; b < kClasses; ++b) sm.hist[b] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    __syncthreads();
-    const int r = sm.item[0];
-    if (r < 0) return;
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(ptx::smem_u32(&sm.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -230,42 +236,151 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     __syncthreads();
     fence_after();
     const uint32_t tmem = sm.tmem;
-
-    const int q0 = a.cu_q[r], nq = a.cu_q[r + 1] - q0, k0 = a.cu_k[r], nk = a.cu_k[r + 1] - k0;
-    const int tok0 = sm.item[1] * 2 * toks, back = nk - nq;          // first token of tile 0; query i sees keys <= back + i
-    // key tiles of each query tile: up to the last key its last token sees
-    int nt[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int first = tok0 + t * toks, last = min(nq, first + toks) - 1;
-        nt[t] = last < first || back + last < 0 ? 0 : (back + last) / kN + 1;
+    // The classes of work: items of x key tiles are class x / width.
+    int most = 0;
+    for (int r = tid; r < a.R; r += kThreads) {
+        const Req q = request(a, r);
+        if (q.nq < 0 && blockIdx.x == 0 && a.err) atomicOr(a.err, LORA_DEV_ERR_BAD_LENGTH);
+        if (q.nq > 0) most = max(most, tiles_to(q, q.nq - 1));
     }
-    const int total = max(nt[0], nt[1]);
-    const int tail_rows = nk - (total - 1) * kN;                     // rows of the last key tile that are the request's (maybe more than kN)
-    const int head = hb * a.pk, kvh = head / a.G;
+    if (most > 0) atomicMax(&sm.most, most);
+    __syncthreads();
+    const int width = sm.most / kClasses + 1;
+    for (int r = tid; r < a.R; r += kThreads) {
+        const Req q = request(a, r);
+        if (q.nq <= 0) continue;
+        int from = 0;
+        for (int b = 0; b < kClasses; ++b) {
+            const int to = b + 1 == kClasses ? (q.nq - 1 >> sh) + 1 : first_pair(q, (b + 1) * width, sh);
+            if (to > from) atomicAdd(&sm.hist[b], to - from);
+            from = to;
+        }
+    }
+    __syncthreads();
 
-    if (warp == 0) {
-        if (lane == 0 && total > 0) {
-            ptx::mbar_expect_tx(&sm.q_full, 2 * TILE);
-            for (int t = 0; t < 2; ++t)
-                for (int h = 0; h < HALVES; ++h)
-                    ptx::tma_load_3d(sm.q[t] + h * HALF, &maps.q, h * 64, head, q0 + tok0 + t * toks, &sm.q_full);
-            int i = 0;
-            for (; i < 2 * total; ++i) {
-                const int s = i % ST;
-                if (i >= ST && !wait(&sm.empty[s], (i / ST - 1) & 1, sm, a.err)) break;
-                ptx::mbar_expect_tx(&sm.full[s], TILE);
-                for (int h = 0; h < HALVES; ++h)
-                    ptx::tma_load_3d(sm.kv[s] + h * HALF, (i & 1) ? &maps.v : &maps.k, h * 64, kvh, k0 + (i >> 1) * kN, &sm.full[s]);
+    // Every role reads the items in order.
+    uint32_t items = 0;
+    const auto next_item = [&](Item &it) {
+        const int s = items & 1;
+        bool ok = wait(&sm.item_full[s], (items >> 1) & 1, sm, a.err);
+        ok = __all_sync(~0u, ok);
+        if (ok) it = sm.item[s];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.item_empty[s]);
+        ++items;
+        return ok && it.nq >= 0;
+    };
+    // Key tiles of each query tile: up to the last key its last token sees.
+    const auto key_tiles = [&](const Item &it, int t) {
+        const int first = it.tok0 + t * toks, last = min(it.nq, first + toks) - 1, key = it.nk - it.nq + last;
+        return last < first || key < 0 ? 0 : key / kN + 1;
+    };
+
+    // Registers go to the row owners: 128 x (88 + 2 x 208) is what the block was launched with, 384 x 168 (checked by the host).
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 3) {
+            int cls = kClasses - 1, r0 = 0;       // where the list is: class, block of 32 requests,
+            long long before = 0;                 // pairs listed before this block
+            int cnt = 0, run = 0, lo = 0;         // this lane's request: pairs in the class, their inclusive sum, the first of them
+            Req q{};
+            bool fresh = true;
+            uint32_t n = 0;
+            for (;; ++n) {
+                // every other round of items backwards: a CTA's largest item of one round goes with its smallest of the next
+                const long long k = (long long)n * gridDim.x + ((n & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                const long long want = k / a.groups;
+                Item it{0, -1, 0, 0, 0, 0};
+                while (cls >= 0) {
+                    if (r0 == 0 && fresh && before + sm.hist[cls] <= want) {   // the class as a whole is behind
+                        before += sm.hist[cls];
+                        --cls;
+                        continue;
+                    }
+                    if (fresh) {
+                        const int r = r0 + lane;
+                        cnt = 0;
+                        if (r < a.R) {
+                            q = request(a, r);
+                            if (q.nq > 0) {
+                                lo = first_pair(q, cls * width, sh);
+                                cnt = (cls + 1 == kClasses ? (q.nq - 1 >> sh) + 1 : first_pair(q, (cls + 1) * width, sh)) - lo;
+                            }
+                        }
+                        run = cnt;
+#pragma unroll
+                        for (int d = 1; d < 32; d <<= 1) {
+                            const int x = __shfl_up_sync(~0u, run, d);
+                            if (lane >= d) run += x;
+                        }
+                        fresh = false;
+                    }
+                    const uint32_t hit = __ballot_sync(~0u, before + run > want);
+                    if (hit) {
+                        const int l = __ffs(hit) - 1;
+                        const int pair = lo + (int)(before + run - 1 - want);   // the longest rows of a request first
+                        it.q0 = __shfl_sync(~0u, q.q0, l);
+                        it.nq = __shfl_sync(~0u, q.nq, l);
+                        it.k0 = __shfl_sync(~0u, q.k0, l);
+                        it.nk = __shfl_sync(~0u, q.nk, l);
+                        it.tok0 = __shfl_sync(~0u, pair, l) << sh;
+                        it.head = (int)(k - want * a.groups) * a.pk;
+                        break;
+                    }
+                    before += __shfl_sync(~0u, run, 31);
+                    r0 += 32;
+                    fresh = true;
+                    if (r0 >= a.R) {
+                        r0 = 0;
+                        --cls;
+                    }
+                }
+                const int s = n & 1;
+                bool ok = n < 2 || wait(&sm.item_empty[s], (n / 2 - 1) & 1, sm, a.err);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    sm.item[s] = it;
+                    ptx::mbar_arrive(&sm.item_full[s]);
+                }
+                if (it.nq < 0) break;
             }
-            if (*(volatile int *)&sm.abort) {   // loads in flight land before the CTA goes
-                drain_wait(&sm.q_full, 0);
+        } else if (warp == 0) {
+            Item it;
+            int i = 0, qn[2] = {0, 0};
+            bool ok = true;
+            while (ok && next_item(it)) {
+                const int nt0 = key_tiles(it, 0), nt1 = key_tiles(it, 1), total = max(nt0, nt1), kvh = it.head / a.G;
+                if (lane == 0) {
+                    for (int j = 0; ok && j < 2 * total; ++j) {
+                        const int s = i % ST;
+                        ok = i < ST || wait(&sm.empty[s], (i / ST - 1) & 1, sm, a.err);
+                        if (!ok) break;
+                        ptx::mbar_expect_tx(&sm.full[s], TILE);
+                        for (int h = 0; h < HALVES; ++h)
+                            ptx::tma_load_3d(sm.kv[s] + h * HALF, (j & 1) ? &maps.v : &maps.k, h * 64, kvh, it.k0 + (j >> 1) * kN, &sm.full[s]);
+                        ++i;
+                        if (j > 0) continue;
+                        for (int t = 0; ok && t < 2; ++t) {   // behind the first keys: these do not wait for the last item's scores
+                            if ((t ? nt1 : nt0) == 0) continue;
+                            ok = qn[t] == 0 || wait(&sm.q_empty[t], (qn[t] - 1) & 1, sm, a.err);
+                            if (!ok) break;
+                            ++qn[t];
+                            ptx::mbar_expect_tx(&sm.q_full[t], TILE);
+                            for (int h = 0; h < HALVES; ++h)
+                                ptx::tma_load_3d(sm.q[t] + h * HALF, &maps.q, h * 64, it.head, it.q0 + it.tok0 + t * toks, &sm.q_full[t]);
+                        }
+                    }
+                }
+                ok = __shfl_sync(~0u, (int)ok, 0);
+            }
+            if (lane == 0 && *(volatile int *)&sm.abort) {   // loads in flight land before the CTA goes
+                for (int t = 0; t < 2; ++t)
+                    if (qn[t] > 0) drain_wait(&sm.q_full[t], (qn[t] - 1) & 1);
                 for (int j = max(0, i - ST); j < i; ++j) drain_wait(&sm.full[j % ST], (j / ST) & 1);
             }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (total > 0) {
+            __syncwarp();
+        } else if (warp == 1) {
             constexpr uint32_t id_s = idesc(BF ? 1 : 0, kN, 0), id_o = idesc(BF ? 1 : 0, DIM, 1);
             const auto scores = [&](int t, int s) {   // one lane
                 const uint64_t dq = sdesc(ptx::smem_u32(sm.q[t]), 16, 1024), dk = sdesc(ptx::smem_u32(sm.kv[s]), 16, 1024);
@@ -277,82 +392,108 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 commit(&sm.s_full[t]);
             };
             const auto await = [&](uint64_t *b, uint32_t parity) { return (bool)__all_sync(~0u, wait(b, parity, sm, a.err)); };
-            bool ok = await(&sm.q_full, 0) && await(&sm.full[0], 0);
-            if (ok && lane == 0) {
-                fence_after();
-                for (int t = 0; t < 2; ++t)
-                    if (nt[t] > 0) scores(t, 0);
-                commit(&sm.empty[0]);
-            }
-            for (int j = 0; ok && j < total; ++j) {
-                const int vs = (2 * j + 1) % ST, ks = (2 * j + 2) % ST;
-                ok = await(&sm.full[vs], ((2 * j + 1) / ST) & 1);
-                if (ok && j == total - 1 && tail_rows < kN) {
-                    // values behind the request's last key: other rows, whatever they hold; 0 x NaN would reach this request
-                    for (int x = tail_rows * 8 + lane; x < kN * 8; x += 32)
-                        for (int h = 0; h < HALVES; ++h)
-                            *reinterpret_cast<uint4 *>(sm.kv[vs] + h * HALF + x * 16) = make_uint4(0, 0, 0, 0);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                }
-                if (ok && j + 1 < total) ok = await(&sm.full[ks], ((2 * j + 2) / ST) & 1);
-                const uint64_t dv = sdesc(ptx::smem_u32(sm.kv[vs]), HALF, 1024);
-                for (int t = 0; ok && t < 2; ++t) {
-                    if (j >= nt[t]) continue;
-                    ok = await(&sm.p_ready[t], j & 1);
+            Item it;
+            int i = 0;                        // ring position of the item's first keys
+            uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};
+            bool ok = true;
+            while (ok && next_item(it)) {
+                const int nt[2] = {key_tiles(it, 0), key_tiles(it, 1)}, total = max(nt[0], nt[1]);
+                if (total == 0) continue;
+                const int tail_rows = it.nk - (total - 1) * kN;   // rows of the last key tile that are the request's (maybe more than kN)
+                ok = await(&sm.full[i % ST], (i / ST) & 1);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (!ok || nt[t] == 0) continue;
+                    ok = await(&sm.q_full[t], qn[t] & 1);
+                    ++qn[t];
                     if (ok && lane == 0) {
                         fence_after();
-#pragma unroll
-                        for (int k = 0; k < kN / 16; ++k)
-                            mma_ts(tmem + 2 * kN + t * 128, tmem + t * kN + k * 8, dv + (uint64_t)(k * (2048 >> 4)), id_o, j != 0 || k != 0);
-                        if (j + 1 < nt[t]) scores(t, ks);
-                        else commit(&sm.o_full[t]);
+                        scores(t, i % ST);
+                        if (nt[t] == 1) commit(&sm.q_empty[t]);
                     }
                 }
-                if (ok && lane == 0) {
-                    commit(&sm.empty[vs]);
-                    if (j + 1 < total) commit(&sm.empty[ks]);
+                if (ok && lane == 0) commit(&sm.empty[i % ST]);
+                for (int j = 0; ok && j < total; ++j) {
+                    const int vi = i + 2 * j + 1, ki = vi + 1, vs = vi % ST, ks = ki % ST;
+                    ok = await(&sm.full[vs], (vi / ST) & 1);
+                    if (ok && j == total - 1 && tail_rows < kN) {
+                        // values behind the request's last key: other rows, whatever they hold; 0 x NaN would reach this request
+                        for (int x = tail_rows * 8 + lane; x < kN * 8; x += 32)
+                            for (int h = 0; h < HALVES; ++h)
+                                *reinterpret_cast<uint4 *>(sm.kv[vs] + h * HALF + x * 16) = make_uint4(0, 0, 0, 0);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                    if (ok && j + 1 < total) ok = await(&sm.full[ks], (ki / ST) & 1);
+                    const uint64_t dv = sdesc(ptx::smem_u32(sm.kv[vs]), HALF, 1024);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (!ok || j >= nt[t]) continue;
+                        ok = await(&sm.p_ready[t], pn[t] & 1);
+                        ++pn[t];
+                        if (ok && lane == 0) {
+                            fence_after();
+#pragma unroll
+                            for (int k = 0; k < kN / 16; ++k)
+                                mma_ts(tmem + 2 * kN + t * 128, tmem + t * kN + k * 8, dv + (uint64_t)(k * (2048 >> 4)), id_o, j != 0 || k != 0);
+                            if (j + 1 < nt[t]) {
+                                scores(t, ks);
+                                if (j + 2 == nt[t]) commit(&sm.q_empty[t]);
+                            } else {
+                                commit(&sm.o_full[t]);
+                            }
+                        }
+                    }
+                    if (ok && lane == 0) {
+                        commit(&sm.empty[vs]);
+                        if (j + 1 < total) commit(&sm.empty[ks]);
+                    }
                 }
+                i += 2 * total;
             }
             if (lane == 0) {
                 commit(&sm.drain);
                 drain_wait(&sm.drain, 0);   // no product runs when the CTA goes
             }
+            __syncwarp();
         }
-        __syncwarp();
-    } else if (warp >= 4) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int t = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // the warp's 32 lanes of tensor memory
         const uint32_t ts = tmem + t * kN + lanes, to = tmem + 2 * kN + t * 128 + lanes;
-        const int tok = tok0 + t * toks + row / a.pk, hq = head + row % a.pk;
-        const bool mine = tok < nq;
-        const int lim = min(back + tok, nk - 1);                      // last key this row sees
-        const int least = min(back + tok0 + t * toks, nk - 1);        // of the tile's first row
         const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f), jump = kJump / c;
         const bool neg = a.scale < 0.f;
-        float m = -INFINITY, mc = -kShift, thr = -INFINITY, l = 0.f;
+        Item it;
+        uint32_t sn = 0, on = 0;
         bool ok = true;
-        for (int j = 0; j < nt[t]; ++j) {
-            ok = wait(&sm.s_full[t], j & 1, sm, a.err);
-            if (!__all_sync(~0u, ok)) break;
-            fence_after();
-            const bool edge = j * kN + kN - 1 > least;
-            float x[4][32];
+        while (ok && next_item(it)) {
+            const int nt = key_tiles(it, t), back = it.nk - it.nq;
+            const int tok = it.tok0 + t * toks + row / a.pk, hq = it.head + row % a.pk;
+            const bool mine = tok < it.nq;
+            const int lim = min(back + tok, it.nk - 1);                      // last key this row sees
+            const int least = min(back + it.tok0 + t * toks, it.nk - 1);     // of the tile's first row
+            float m = -INFINITY, mc = -kShift, thr = -INFINITY, l = 0.f;
+            for (int j = 0; j < nt; ++j, ++sn) {
+                ok = wait(&sm.s_full[t], sn & 1, sm, a.err);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                fence_after();
+                const bool edge = j * kN + kN - 1 > least;
+                float x[4][32];
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) ld32(x[ch], ts + ch * 32);
-            wait_ld();
-            if (neg) {
+                for (int ch = 0; ch < 4; ++ch) ld32(x[ch], ts + ch * 32);
+                wait_ld();
+                if (neg) {
 #pragma unroll
-                for (int e = 0; e < kN; ++e) x[e / 32][e % 32] = -x[e / 32][e % 32];
-            }
-            if (edge) {
-                const int from = lim - j * kN;
+                    for (int e = 0; e < kN; ++e) x[e / 32][e % 32] = -x[e / 32][e % 32];
+                }
+                if (edge) {
+                    const int from = lim - j * kN;
 #pragma unroll
-                for (int e = 0; e < kN; ++e)
-                    if (e > from) x[e / 32][e % 32] = -INFINITY;
-            }
-            float top = -INFINITY;
-            {
+                    for (int e = 0; e < kN; ++e)
+                        if (e > from) x[e / 32][e % 32] = -INFINITY;
+                }
                 float u[4];
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
@@ -361,81 +502,81 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     for (int e = 1; e < 31; e += 2) u[ch] = fmaxf(u[ch], fmaxf(x[ch][e], x[ch][e + 1]));
                     u[ch] = fmaxf(u[ch], x[ch][31]);
                 }
-                top = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3]));
-            }
-            const bool up = top > thr;
-            if (__any_sync(~0u, up)) {
-                const float n = up ? top : m;
-                const float f = !up ? 1.f : m == -INFINITY ? 0.f : ex2((m - n) * c);
-                m = n;
-                mc = (n == -INFINITY ? 0.f : n * c) - kShift;
-                thr = n + jump;
-                l *= f;
-                if (j > 0) {
+                const float top = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3]));
+                const bool up = top > thr;
+                if (__any_sync(~0u, up)) {
+                    const float n = up ? top : m;
+                    const float f = !up ? 1.f : m == -INFINITY ? 0.f : ex2((m - n) * c);
+                    m = n;
+                    mc = (n == -INFINITY ? 0.f : n * c) - kShift;
+                    thr = n + jump;
+                    l *= f;
+                    if (j > 0) {
 #pragma unroll 1
-                    for (int ch = 0; ch < DIM / 32; ++ch) {
-                        float o[32];
-                        ld32(o, to + ch * 32);
-                        wait_ld();
-                        uint32_t u[32];
+                        for (int ch = 0; ch < DIM / 16; ++ch) {
+                            float o[16];
+                            ld16(o, to + ch * 16);
+                            wait_ld();
+                            uint32_t w[16];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
-                        st32(to + ch * 32, u);
+                            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
+                            st16(to + ch * 16, w);
+                        }
                     }
                 }
-            }
-            const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
-            float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
+                const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+                float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-                uint32_t p[16];
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t p[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float2 y = fma2(make_float2(x[ch][2 * e], x[ch][2 * e + 1]), c2, mc2);
-                    const float2 w = make_float2(ex2(y.x), ex2(y.y));
-                    sum[e & 1] = add2(sum[e & 1], w);
-                    p[e] = pack<BF>(w.x, w.y);
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 y = fma2(make_float2(x[ch][2 * e], x[ch][2 * e + 1]), c2, mc2);
+                        const float2 w = make_float2(ex2(y.x), ex2(y.y));
+                        sum[e & 1] = add2(sum[e & 1], w);
+                        p[e] = pack<BF>(w.x, w.y);
+                    }
+                    st16(ts + ch * 16, p);
                 }
-                st16(ts + ch * 16, p);
+                l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sm.p_ready[t]);
             }
-            l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&sm.p_ready[t]);
-        }
-        ok = __all_sync(~0u, ok);
-        if (ok && nt[t] > 0) {
-            ok = wait(&sm.o_full[t], 0, sm, a.err);
-            ok = __all_sync(~0u, ok);
-            fence_after();
-        }
-        if (ok) {
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            H *out = reinterpret_cast<H *>(a.o) + (long long)(q0 + tok) * a.ots + (long long)hq * a.ohs;
+            if (ok && nt > 0) {
+                ok = wait(&sm.o_full[t], on & 1, sm, a.err);
+                ok = __all_sync(~0u, ok);
+                ++on;
+                fence_after();
+            }
+            if (!ok) break;
+            const bool none = l == 0.f;
+            const float inv = none ? 0.f : 1.f / l;
+            H *out = reinterpret_cast<H *>(a.o) + (long long)(it.q0 + tok) * a.ots + (long long)hq * a.ohs;
 #pragma unroll 1
             for (int ch = 0; ch < DIM / 32; ++ch) {
                 float o[32];
-                if (nt[t] > 0) {
+                if (nt > 0) {
                     ld32(o, to + ch * 32);
                     wait_ld();
                 }
                 if (mine) {
-                    const bool none = l == 0.f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        uint4 u = make_uint4(0, 0, 0, 0);
+                        uint4 w = make_uint4(0, 0, 0, 0);
                         if (!none) {
-                            u.x = pack<BF>(o[8 * i] * inv, o[8 * i + 1] * inv);
-                            u.y = pack<BF>(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
-                            u.z = pack<BF>(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
-                            u.w = pack<BF>(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
+                            w.x = pack<BF>(o[8 * i] * inv, o[8 * i + 1] * inv);
+                            w.y = pack<BF>(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
+                            w.z = pack<BF>(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
+                            w.w = pack<BF>(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
                         }
-                        *reinterpret_cast<uint4 *>(out + ch * 32 + 8 * i) = u;
+                        *reinterpret_cast<uint4 *>(out + ch * 32 + 8 * i) = w;
                     }
                 }
             }
-            if (a.lse && mine) a.lse[(size_t)(q0 + tok) * a.hq + hq] = l == 0.f ? -INFINITY : 0.6931471805599453f * (mc + log2f(l));
+            fence_before();   // the next item's products may write over these outputs
+            if (a.lse && mine) a.lse[(size_t)(it.q0 + tok) * a.hq + hq] = none ? -INFINITY : 0.6931471805599453f * (mc + log2f(l));
         }
     }
 
@@ -463,7 +604,6 @@ int launch(const PromptArgs &a, cudaStream_t st) {
     k.groups = a.hq / k.pk;
     const int pair = 2 * kM / k.pk;                                     // tokens of a CTA
     const long long items = ((long long)a.Tq / pair + a.R) * k.groups;  // at least the tile pairs of any row ranges
-    if (items > INT32_MAX) return LORA_ERR_TOO_LARGE;
     Maps maps;
     // without keys nothing is loaded: any valid address serves
     const Rows kr = a.Tk > 0 ? a.k : a.q, vr = a.Tk > 0 ? a.v : a.q;
@@ -473,7 +613,14 @@ int launch(const PromptArgs &a, cudaStream_t st) {
     const size_t smem = sizeof(Smem<DIM>) + 1024;
     static_assert(sizeof(Smem<DIM>) + 1024 <= 227 * 1024, "prompt kernel: shared memory beyond the per-block limit");
     if (int rc = cuda_check(cudaFuncSetAttribute(prompt_kernel<DIM, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))) return rc;
-    prompt_kernel<DIM, BF><<<(int)items, kThreads, smem, st>>>(maps, k);
+    static_assert(kThreads * 168 == 128 * (88 + 2 * 208), "register split");
+    cudaFuncAttributes fa;
+    if (int rc = cuda_check(cudaFuncGetAttributes(&fa, prompt_kernel<DIM, BF>))) return rc;
+    if (fa.numRegs != 168) return LORA_ERR_CUDA;   // the row owners would wait for registers that the block does not have
+    int dev = 0, sms = 0;
+    if (int rc = cuda_check(cudaGetDevice(&dev))) return rc;
+    if (int rc = cuda_check(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev))) return rc;
+    prompt_kernel<DIM, BF><<<(int)(items < sms ? items : sms), kThreads, smem, st>>>(maps, k);
     count_launch();
     return cuda_check(cudaGetLastError());
 }
