@@ -1,5 +1,7 @@
 // C-ABI entry points of the KV-cache and attention calls: argument checks, then
 // one launcher each.  See include/lora.h for the contract of every function.
+#include <cmath>
+
 #include "lora_internal.cuh"
 #include "lora_kv.cuh"
 
@@ -167,7 +169,7 @@ int lora_prompt_attend(const lora_rows_t *q, const lora_rows_t *k, const lora_ro
                        float scale, const lora_rows_t *out, float *lse, int32_t *err_dev, lora_stream_t stream) {
     reset_launch_count();
     if (!half_type(dtype) || Tq < 0 || Tk < 0 || R < 1 || !group_ok(q_heads, kv_heads) ||
-        (head_dim != 64 && head_dim != 128) || !cu_q || !cu_k)
+        (head_dim != 64 && head_dim != 128) || !cu_q || !cu_k || !(scale >= 0.f && scale < INFINITY))
         return LORA_ERR_INVALID_ARG;
     if (R > LORA_KV_MAX_REQUESTS) return LORA_ERR_TOO_LARGE;
     if (Tq == 0) return LORA_OK;

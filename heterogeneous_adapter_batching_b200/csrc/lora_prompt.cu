@@ -147,12 +147,16 @@ __device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
                  ::"r"(addr), W8(r, 0), W8(r, 8) : "memory");
 }
+__device__ __forceinline__ void st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+                 "%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr), W8(r, 0), W8(r, 8), W8(r, 16), W8(r, 24) : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// Two fp32 operations an instruction.
+// Two fp32 operations an instruction (the same rate of operations, half the issue slots).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
     asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     extern __shared__ unsigned char raw[];
     Smem<DIM> &sm = *reinterpret_cast<Smem<DIM> *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int toks = kM / a.pk, sh = __ffs(toks);              // tokens of a tile; log2 of those of a pair
+    const int toks = kM / a.pk, sh = __ffs(toks), lpk = __ffs(a.pk) - 1;   // tokens of a tile; log2 of a pair's, of the heads'
 
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
@@ -462,14 +466,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const int t = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // the warp's 32 lanes of tensor memory
         const uint32_t ts = tmem + t * kN + lanes, to = tmem + 2 * kN + t * 128 + lanes;
-        const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f), jump = kJump / c;
-        const bool neg = a.scale < 0.f;
+        const float c = fmaxf(a.scale * 1.4426950408889634f, 1e-37f), jump = kJump / c;
         Item it;
         uint32_t sn = 0, on = 0;
+        const bool wide = (((uintptr_t)a.o | (uintptr_t)(a.ots * 2) | (uintptr_t)(a.ohs * 2)) & 31) == 0;
         bool ok = true;
         while (ok && next_item(it)) {
             const int nt = key_tiles(it, t), back = it.nk - it.nq;
-            const int tok = it.tok0 + t * toks + row / a.pk, hq = it.head + row % a.pk;
+            const int tok = it.tok0 + t * toks + (row >> lpk), hq = it.head + (row & (a.pk - 1));
             const bool mine = tok < it.nq;
             const int lim = min(back + tok, it.nk - 1);                      // last key this row sees
             const int least = min(back + it.tok0 + t * toks, it.nk - 1);     // of the tile's first row
@@ -479,21 +483,25 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
                 fence_after();
-                const bool edge = j * kN + kN - 1 > least;
+                // Scores of keys that some row does not see are masked where they are: the code of the other tiles stays small.
+                if (j * kN + kN - 1 > least) {
+                    const int from = lim - j * kN;
+#pragma unroll 1
+                    for (int ch = 0; ch < 4; ++ch) {
+                        float s[32];
+                        ld32(s, ts + ch * 32);
+                        wait_ld();
+                        uint32_t w[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) w[e] = ch * 32 + e > from ? 0xff800000u : __float_as_uint(s[e]);
+                        st32(ts + ch * 32, w);
+                    }
+                    wait_st();
+                }
                 float x[4][32];
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) ld32(x[ch], ts + ch * 32);
                 wait_ld();
-                if (neg) {
-#pragma unroll
-                    for (int e = 0; e < kN; ++e) x[e / 32][e % 32] = -x[e / 32][e % 32];
-                }
-                if (edge) {
-                    const int from = lim - j * kN;
-#pragma unroll
-                    for (int e = 0; e < kN; ++e)
-                        if (e > from) x[e / 32][e % 32] = -INFINITY;
-                }
                 float u[4];
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
@@ -524,19 +532,23 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                         }
                     }
                 }
+                // Weights, as a pipeline over the 64 pairs of the row: exponents two pairs ahead of the exponentials, sums and
+                // packing four pairs behind them.
                 const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
                 float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
+                float2 y[kN / 2];
+                uint32_t p[16];
+                constexpr int kAhead = 2, kLag = 4;
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 y = fma2(make_float2(x[ch][2 * e], x[ch][2 * e + 1]), c2, mc2);
-                        const float2 w = make_float2(ex2(y.x), ex2(y.y));
-                        sum[e & 1] = add2(sum[e & 1], w);
-                        p[e] = pack<BF>(w.x, w.y);
+                for (int i = -kAhead; i < kN / 2 + kLag; ++i) {
+                    const int n = i + kAhead, k = i - kLag;
+                    if (n < kN / 2) y[n] = fma2(make_float2(x[n / 16][n % 16 * 2], x[n / 16][n % 16 * 2 + 1]), c2, mc2);
+                    if (i >= 0 && i < kN / 2) y[i] = make_float2(ex2(y[i].x), ex2(y[i].y));
+                    if (k >= 0) {
+                        sum[k & 1] = add2(sum[k & 1], y[k]);
+                        p[k % 16] = pack<BF>(y[k].x, y[k].y);
+                        if (k % 16 == 15) st16(ts + k / 16 * 16, p);
                     }
-                    st16(ts + ch * 16, p);
                 }
                 l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 wait_st();
@@ -563,15 +575,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 }
                 if (mine) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint4 w = make_uint4(0, 0, 0, 0);
-                        if (!none) {
-                            w.x = pack<BF>(o[8 * i] * inv, o[8 * i + 1] * inv);
-                            w.y = pack<BF>(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
-                            w.z = pack<BF>(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
-                            w.w = pack<BF>(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
+                    for (int i = 0; i < 2; ++i) {   // a whole 32-byte sector at a time where rows lie so
+                        uint32_t w[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w[e] = none ? 0u : pack<BF>(o[16 * i + 2 * e] * inv, o[16 * i + 2 * e + 1] * inv);
+                        H *at = out + ch * 32 + 16 * i;
+                        if (wide) {
+                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), W8(w, 0) : "memory");
+                        } else {
+                            reinterpret_cast<uint4 *>(at)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            reinterpret_cast<uint4 *>(at)[1] = make_uint4(w[4], w[5], w[6], w[7]);
                         }
-                        *reinterpret_cast<uint4 *>(out + ch * 32 + 8 * i) = w;
                     }
                 }
             }

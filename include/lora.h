@@ -562,8 +562,8 @@ int lora_kv_attend(const lora_rows_t *q, int T, int q_heads, int dtype, const lo
  * prefix comes from the cache (lora_kv_gather).
  *   q, out [Tq][q_heads], k, v [Tk][kv_heads] rows of dtype (LORA_BF16 or
  *   LORA_FP16), head_dim 64 or 128; strides of q, k and v are positive (where
- *   there is more than one token or head) and below 2^40 bytes; lse
- *   [Tq][q_heads] fp32 or NULL.  cu_q, cu_k
+ *   there is more than one token or head) and below 2^40 bytes; scale is
+ *   finite and not negative; lse [Tq][q_heads] fp32 or NULL.  cu_q, cu_k
  *   [R+1] int32 on the device, not decreasing, within [0, Tq] and [0, Tk]: a
  *   request that is not sets LORA_DEV_ERR_BAD_LENGTH and its rows are left alone.
  * Rows outside [cu_q[0], cu_q[R]) are left alone.  A row that attends to nothing

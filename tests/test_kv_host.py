@@ -128,15 +128,17 @@ def test_attend_refusals(H):
 def test_prompt_refusals(H):
     lib = H.load_library()
 
-    def call(q=None, k=None, v=None, Tq=4, Tk=4, hq=32, hk=8, dim=128, dtype=0, cq=p(), ck=p(), R=1, out=None):
+    def call(q=None, k=None, v=None, Tq=4, Tk=4, hq=32, hk=8, dim=128, dtype=0, cq=p(), ck=p(), R=1, out=None, scale=1.0):
         q, k, v, out = (rows(H) if x is None else x for x in (q, k, v, out))
-        return lib.lora_prompt_attend(q, k, v, Tq, Tk, hq, hk, dim, dtype, cq, ck, R, 1.0, out, None, None, None)
+        return lib.lora_prompt_attend(q, k, v, Tq, Tk, hq, hk, dim, dtype, cq, ck, R, scale, out, None, None, None)
 
     assert call(Tq=0) == 0
     assert call(Tq=-1) == -1 and call(Tk=-1) == -1 and call(R=0) == -1 and call(cq=None) == -1 and call(ck=None) == -1
     assert call(hq=31) == -1 and call(hk=0) == -1 and call(dim=96) == -1 and call(dim=256) == -1 and call(dtype=2) == -1
     assert call(k=rows(H, 8)) == -1 and call(v=rows(H, ts=1026)) == -1 and call(out=rows(H, hs=-128)) == -1
     assert call(R=4097) == -8
+    assert call(scale=-1.0) == -1 and call(scale=float("nan")) == -1 and call(scale=float("inf")) == -1
+    assert call(q=rows(H, ts=0)) == -1 and call(k=rows(H, hs=0)) == -1 and call(v=rows(H, ts=1 << 39)) == -1   # what a descriptor takes
     assert lib.lora_last_launch_count() == 0
 
 
