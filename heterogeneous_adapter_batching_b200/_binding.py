@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -379,72 +380,86 @@ class SlotCache:
         return h.value, m.value, e.value
 
 
+# The calls below run once per layer and step, some of them for a few microseconds: their checks are plain attribute
+# comparisons, pointers go as integers and row tensors as packed lora_rows_t.
+_ROWS = struct.Struct("=Qqq")                 # lora_rows_t
+_KV = struct.Struct("=QQiiii")                # lora_kv_cache_t
+
+
 def _refuse(name: str, why: str):
     raise LoraError(name, -1, why)
 
 
-def _row_tensors(name: str, *tensors):
-    """Check [T, heads, head_dim] tensors (None: absent): one device, rows whose
-    elements are adjacent."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if t.dim() != 3 or not t.is_cuda or t.dtype not in DTYPES:
-            _refuse(name, "row tensors are CUDA tensors [T, heads, head_dim] of bf16, fp16 or fp32")
-        if t.stride(2) != 1 and t.shape[2] > 1:
-            _refuse(name, "the elements of a row are adjacent")
-        if dev is not None and t.device != dev:
-            _refuse(name, "tensors on different devices")
-        dev = t.device
+def _device(name: str, t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        _refuse(name, "tensors of a CUDA device are expected")
     return dev
 
 
-def _ints(name: str, dev, n, *tensors):
-    """Check contiguous int32 tensors on `dev` with at least n elements (None: absent)."""
-    for t in tensors:
-        if t is None:
-            continue
-        if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous() or t.numel() < n:
-            _refuse(name, f"index arrays are contiguous int32 tensors on {dev} with at least {n} elements")
+def _r(name: str, t: Optional[torch.Tensor], dev: int, dtype, dim: int):
+    """lora_rows_t of a [T, heads, head_dim] tensor (None: a null pointer)."""
+    if t is None:
+        return None
+    n, s = t.shape, t.stride()
+    if len(n) != 3 or n[2] != dim or t.dtype != dtype or t.get_device() != dev:
+        _refuse(name, f"rows [T, heads, {dim}] of {dtype} on cuda:{dev} expected, not {tuple(n)} of {t.dtype} on {t.device}")
+    if s[2] != 1:
+        _refuse(name, "the elements of a row are adjacent")
+    # the stride of a dimension of one element says nothing
+    return _ROWS.pack(t.data_ptr(), s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0)
+
+
+def _i(name: str, t: Optional[torch.Tensor], dev: int, n: int):
+    """Address of a contiguous int32 tensor of at least n elements (None: a null pointer)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
+        _refuse(name, f"index arrays are contiguous int32 tensors on cuda:{dev} with at least {n} elements")
+    return t.data_ptr()
 
 
 def _same(name: str, what: str, a, b):
     if a != b:
-        _refuse(name, f"{what}: {tuple(a) if isinstance(a, torch.Size) else a} against {tuple(b) if isinstance(b, torch.Size) else b}")
+        _refuse(name, f"{what}: {a} against {b}")
 
 
-def _r(t: Optional[torch.Tensor]):
-    """lora_rows_t of a tensor (None: a null pointer)."""
-    if t is None:
-        return None
-    n, s = t.shape, t.stride()   # the stride of a dimension of one element says nothing
-    return ctypes.byref(LoraRows(t.data_ptr(), s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0))
-
-
-def _kv(name: str, pages: torch.Tensor, kv_heads: int, head_dim: int, block_tokens: int):
+def _kv(name: str, pages: torch.Tensor, dev: int, kv_heads: int, head_dim: int, block_tokens: int):
     """lora_kv_cache_t over pages [num_pages, page bytes or values], rows contiguous."""
-    if pages.dim() != 2 or not pages.is_cuda or not pages.is_contiguous():
-        _refuse(name, "pages is a contiguous CUDA tensor [num_pages, page]")
-    return ctypes.byref(LoraKvCache(pages.data_ptr(), pages.shape[1] * pages.element_size(), pages.shape[0], kv_heads,
-                                    head_dim, block_tokens))
+    n = pages.shape
+    if len(n) != 2 or pages.get_device() != dev or not pages.is_contiguous():
+        _refuse(name, f"pages is a contiguous tensor [num_pages, page] on cuda:{dev}")
+    return _KV.pack(pages.data_ptr(), n[1] * pages.element_size(), n[0], kv_heads, head_dim, block_tokens)
 
 
-class _On:
-    """Runs a call with the tensors' device current; stream None is that device's current stream."""
+def _freq(name: str, f: Optional[torch.Tensor], dev: int):
+    """(address, rot_dim) of inverse frequencies."""
+    if f is None:
+        return None, 0
+    if f.dtype != torch.float32 or f.get_device() != dev or not f.is_contiguous():
+        _refuse(name, f"inv_freq is a contiguous fp32 tensor on cuda:{dev}")
+    return f.data_ptr(), 2 * f.numel()
 
-    def __init__(self, dev, stream):
-        self.dev, self.stream = dev, stream
 
-    def __enter__(self):
-        self.back = torch.cuda.current_device()
-        if self.dev.index != self.back:
-            torch.cuda.set_device(self.dev)
-        return _s(self.stream)
+def _lse(name, lse, q, dev):
+    if lse is None:
+        return None
+    if lse.dtype != torch.float32 or lse.get_device() != dev or not lse.is_contiguous() or lse.shape != q.shape[:2]:
+        _refuse(name, "lse is a contiguous fp32 tensor [T, q_heads] on the device of q")
+    return lse.data_ptr()
 
-    def __exit__(self, *_):
-        if self.dev.index != self.back:
-            torch.cuda.set_device(self.back)
+
+def _run(name: str, dev: int, stream, *args) -> None:
+    """Call `name` with the tensors' device current, on `stream` (None: that device's current stream)."""
+    fn = getattr(_lib or load_library(), name)
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, st)
+    if rc:
+        _check(name, rc)
 
 
 def lora_kv_block_bytes(kv_heads: int, head_dim: int, block_tokens: int) -> int:
@@ -456,54 +471,32 @@ def lora_kv_layout(past_len, new_len, req_ids, block_tokens: int, block_table, f
     """past_len, new_len, req_ids [R], block_table [R, max_blocks]; cu_new [R + 1], kv_len [R], positions, slots, ids [T]
     out; free_pages None: block_table already names every block."""
     n = "lora_kv_layout"
+    dev = _device(n, past_len)
     if block_table.dim() != 2 or positions.dim() != 1:
         _refuse(n, "block_table is [R, max_blocks], positions [T]")
-    if not past_len.is_cuda:
-        _refuse(n, "past_len is a CUDA tensor")
-    R, T, dev = past_len.numel(), positions.numel(), past_len.device
-    _ints(n, dev, R, past_len, new_len, req_ids, kv_len)
-    _ints(n, dev, R + 1, cu_new)
-    _ints(n, dev, R * block_table.shape[1], block_table)
-    _ints(n, dev, T, positions, slots, ids)
-    _ints(n, dev, 0, free_pages)
-    _ints(n, dev, 1, err)
-    _ints(n, dev, 1, free_head, free_head_out)
-    with _On(dev, stream) as st:
-        _check(n, load_library().lora_kv_layout(
-            _p(past_len), _p(new_len), _p(req_ids), R, T, block_tokens, _p(block_table), block_table.shape[1],
-            _p(free_pages), 0 if free_pages is None else free_pages.numel(), _p(free_head), _p(cu_new), _p(kv_len),
-            _p(positions), _p(slots), _p(ids), _p(free_head_out), _p(err), st))
-
-
-def _rope_args(name, q, k, v, positions, inv_freq, q_out, k_out, v_out, slots=None):
-    dev = _row_tensors(name, q, k, v, q_out, k_out, v_out)
-    first = k if q is None else q
-    for x, y in ((q, q_out), (k, k_out), (v, v_out)):
-        if x is not None and y is not None:
-            _same(name, "input and output shapes", x.shape, y.shape)
-        if x is not None:
-            _same(name, "rows and head_dim", (x.shape[0], x.shape[2], x.dtype), (first.shape[0], first.shape[2], first.dtype))
-    outs = [x.dtype for x in (q_out, k_out, v_out) if x is not None]
-    if any(o != outs[0] for o in outs):
-        _refuse(name, "outputs of different types")
-    _ints(name, dev, first.shape[0], positions, slots)
-    if inv_freq is not None and (inv_freq.dtype != torch.float32 or inv_freq.device != dev or not inv_freq.is_contiguous()):
-        _refuse(name, f"inv_freq is a contiguous fp32 tensor on {dev}")
-    return dev, first, DTYPES[outs[0] if outs else first.dtype]
+    R, T, width = past_len.numel(), positions.numel(), block_table.shape[1]
+    _run(n, dev, stream, _i(n, past_len, dev, R), _i(n, new_len, dev, R), _i(n, req_ids, dev, R), R, T, block_tokens,
+         _i(n, block_table, dev, R * width), width, _i(n, free_pages, dev, 0), 0 if free_pages is None else free_pages.numel(),
+         _i(n, free_head, dev, 1), _i(n, cu_new, dev, R + 1), _i(n, kv_len, dev, R), _i(n, positions, dev, T),
+         _i(n, slots, dev, T), _i(n, ids, dev, T), _i(n, free_head_out, dev, 1), _i(n, err, dev, 1))
 
 
 def lora_rope(q, k, positions, inv_freq, q_out, k_out=None, interleaved: bool = False, mscale: float = 1.0,
               stream=None) -> None:
     """q [T, q_heads, head_dim] (k likewise, or None with k_out None); inv_freq [rot_dim / 2] fp32 on the device."""
     n = "lora_rope"
-    dev, first, dst = _rope_args(n, q, k, None, positions, inv_freq, q_out, k_out, None)
+    dev, src, dst = _device(n, q), q.dtype, q_out.dtype
+    T, hq, dim = q.shape
+    _same(n, "q_out", q_out.shape, q.shape)
     if (k is None) != (k_out is None):
         _refuse(n, "k and k_out come together")
-    with _On(dev, stream) as st:
-        _check(n, load_library().lora_rope(
-            _r(q), q.shape[1], _r(k), 0 if k is None else k.shape[1], DTYPES[q.dtype], q.shape[0], q.shape[2],
-            _p(positions), _p(inv_freq), 0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved), mscale,
-            _r(q_out), _r(k_out), dst, st))
+    if k is not None:
+        _same(n, "k_out", k_out.shape, k.shape)
+        _same(n, "rows of q and k", k.shape[0], T)
+    f, rot = _freq(n, inv_freq, dev)
+    _run(n, dev, stream, _r(n, q, dev, src, dim), hq, _r(n, k, dev, src, dim), 0 if k is None else k.shape[1],
+         DTYPES.get(src, -1), T, dim, _i(n, positions, dev, T), f, rot, int(interleaved), mscale,
+         _r(n, q_out, dev, dst, dim), _r(n, k_out, dev, dst, dim), DTYPES.get(dst, -1))
 
 
 def lora_kv_append(q, k, v, positions, inv_freq, slots, pages, block_tokens: int, q_out, k_out=None, v_out=None,
@@ -511,90 +504,68 @@ def lora_kv_append(q, k, v, positions, inv_freq, slots, pages, block_tokens: int
     """lora_rope on q and k, then k and v into the cache `pages` [num_pages, page].  dtype: the type that is cached and
     written, by default that of the outputs (of k when there is none)."""
     n = "lora_kv_append"
-    dev, first, dst = _rope_args(n, q, k, v, positions, inv_freq, q_out, k_out, v_out, slots)
-    _same(n, "k and v shapes", k.shape, v.shape)
+    dev, src = _device(n, k), k.dtype
+    T, hk, dim = k.shape
+    dst = dtype or next((x.dtype for x in (q_out, k_out, v_out) if x is not None), src)
+    _same(n, "v", v.shape, k.shape)
     if (q is None) != (q_out is None):
         _refuse(n, "q and q_out come together")
-    if dtype is not None:
-        if any(x is not None and x.dtype != dtype for x in (q_out, k_out, v_out)):
-            _refuse(n, "outputs of another type than dtype")
-        dst = DTYPES[dtype]
-    if pages.device != dev:
-        _refuse(n, "pages on another device")
-    _ints(n, dev, 1, err)
-    kv = _kv(n, pages, k.shape[1], k.shape[2], block_tokens)
-    with _On(dev, stream) as st:
-        _check(n, load_library().lora_kv_append(
-            _r(q), 0 if q is None else q.shape[1], _r(k), _r(v), DTYPES[k.dtype], k.shape[0], _p(positions), _p(inv_freq),
-            0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved), mscale, _p(slots), kv, _r(q_out), _r(k_out),
-            _r(v_out), dst, _p(err), st))
+    if q is not None:
+        _same(n, "q_out", q_out.shape, q.shape)
+        _same(n, "rows of q and k", q.shape[0], T)
+    for x in (k_out, v_out):
+        if x is not None:
+            _same(n, "k_out and v_out", x.shape, k.shape)
+    f, rot = _freq(n, inv_freq, dev)
+    _run(n, dev, stream, _r(n, q, dev, src, dim), 0 if q is None else q.shape[1], _r(n, k, dev, src, dim),
+         _r(n, v, dev, src, dim), DTYPES.get(src, -1), T, _i(n, positions, dev, T), f, rot, int(interleaved), mscale,
+         _i(n, slots, dev, T), _kv(n, pages, dev, hk, dim, block_tokens), _r(n, q_out, dev, dst, dim),
+         _r(n, k_out, dev, dst, dim), _r(n, v_out, dev, dst, dim), DTYPES.get(dst, -1), _i(n, err, dev, 1))
 
 
 def lora_kv_gather(pages, block_tokens: int, slots, k_out, v_out=None, err=None, stream=None) -> None:
     """Rows slots[t] of the cache into k_out and v_out [T, kv_heads, head_dim] (either may be None)."""
     n = "lora_kv_gather"
-    dev = _row_tensors(n, k_out, v_out)
     first = v_out if k_out is None else k_out
+    dev, dst = _device(n, first), first.dtype
+    T, hk, dim = first.shape
     if k_out is not None and v_out is not None:
-        _same(n, "k_out and v_out", (k_out.shape, k_out.dtype), (v_out.shape, v_out.dtype))
-    if pages.device != dev:
-        _refuse(n, "pages on another device")
-    _ints(n, dev, first.shape[0], slots)
-    _ints(n, dev, 1, err)
-    kv = _kv(n, pages, first.shape[1], first.shape[2], block_tokens)
-    with _On(dev, stream) as st:
-        _check(n, load_library().lora_kv_gather(kv, _p(slots), first.shape[0], _r(k_out), _r(v_out), DTYPES[first.dtype],
-                                                _p(err), st))
+        _same(n, "v_out", v_out.shape, k_out.shape)
+    _run(n, dev, stream, _kv(n, pages, dev, hk, dim, block_tokens), _i(n, slots, dev, T), T, _r(n, k_out, dev, dst, dim),
+         _r(n, v_out, dev, dst, dim), DTYPES.get(dst, -1), _i(n, err, dev, 1))
 
 
 def lora_kv_attend_workspace_size(q_heads: int, kv_heads: int, head_dim: int, max_q_len: int) -> int:
     return int(load_library().lora_kv_attend_workspace_size(q_heads, kv_heads, head_dim, max_q_len))
 
 
-def _lse(name, lse, q):
-    if lse is not None and (lse.dtype != torch.float32 or lse.device != q.device or not lse.is_contiguous() or
-                            lse.shape != q.shape[:2]):
-        _refuse(name, "lse is a contiguous fp32 tensor [T, q_heads] on the device of q")
-
-
 def lora_kv_attend(q, pages, block_tokens: int, kv_heads: int, block_table, cu_q, kv_len, max_q_len: int, scale: float,
                    out, ws, lse=None, err=None, stream=None) -> None:
     """q, out [T, q_heads, head_dim]; block_table [R, max_blocks], cu_q [R + 1], kv_len [R]."""
     n = "lora_kv_attend"
-    dev = _row_tensors(n, q, out)
-    _same(n, "q and out", (q.shape, q.dtype), (out.shape, out.dtype))
-    if pages.device != dev or ws.device != dev:
-        _refuse(n, "pages or ws on another device")
-    if block_table.dim() != 2:
-        _refuse(n, "block_table is [R, max_blocks]")
+    dev, dt = _device(n, q), q.dtype
+    T, hq, dim = q.shape
+    _same(n, "out", out.shape, q.shape)
+    if block_table.dim() != 2 or ws.get_device() != dev or not ws.is_contiguous():
+        _refuse(n, f"block_table is [R, max_blocks], ws contiguous on cuda:{dev}")
     R, width = block_table.shape
-    _ints(n, dev, R * width, block_table)
-    _ints(n, dev, R, kv_len)
-    _ints(n, dev, R + 1, cu_q)
-    _ints(n, dev, 1, err)
-    _lse(n, lse, q)
-    kv = _kv(n, pages, kv_heads, q.shape[2], block_tokens)
-    with _On(dev, stream) as st:
-        _check(n, load_library().lora_kv_attend(
-            _r(q), q.shape[0], q.shape[1], DTYPES[q.dtype], kv, _p(block_table), width, _p(cu_q), _p(kv_len), R, max_q_len,
-            scale, _r(out), _p(lse), _p(ws), ws.numel() * ws.element_size(), _p(err), st))
+    _run(n, dev, stream, _r(n, q, dev, dt, dim), T, hq, DTYPES.get(dt, -1), _kv(n, pages, dev, kv_heads, dim, block_tokens),
+         _i(n, block_table, dev, R * width), width, _i(n, cu_q, dev, R + 1), _i(n, kv_len, dev, R), R, max_q_len, scale,
+         _r(n, out, dev, dt, dim), _lse(n, lse, q, dev), ws.data_ptr(), ws.numel() * ws.element_size(), _i(n, err, dev, 1))
 
 
 def lora_prompt_attend(q, k, v, cu_q, cu_k, scale: float, out, lse=None, err=None, stream=None) -> None:
     """q, out [Tq, q_heads, head_dim], k, v [Tk, kv_heads, head_dim]; cu_q, cu_k [R + 1]."""
     n = "lora_prompt_attend"
-    dev = _row_tensors(n, q, k, v, out)
-    _same(n, "q and out", (q.shape, q.dtype), (out.shape, out.dtype))
-    _same(n, "k and v", (k.shape, k.dtype), (v.shape, v.dtype))
-    _same(n, "q and k", (q.shape[2], q.dtype), (k.shape[2], k.dtype))
-    _ints(n, dev, 2, cu_q, cu_k)
-    _same(n, "cu_q and cu_k", cu_q.numel(), cu_k.numel())
-    _ints(n, dev, 1, err)
-    _lse(n, lse, q)
-    with _On(dev, stream) as st:
-        _check(n, load_library().lora_prompt_attend(
-            _r(q), _r(k), _r(v), q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2], DTYPES[q.dtype], _p(cu_q),
-            _p(cu_k), cu_q.numel() - 1, scale, _r(out), _p(lse), _p(err), st))
+    dev, dt = _device(n, q), q.dtype
+    T, hq, dim = q.shape
+    _same(n, "out", out.shape, q.shape)
+    _same(n, "v", v.shape, k.shape)
+    R = cu_q.numel() - 1
+    _same(n, "cu_k", cu_k.numel(), R + 1)
+    _run(n, dev, stream, _r(n, q, dev, dt, dim), _r(n, k, dev, dt, dim), _r(n, v, dev, dt, dim), T, k.shape[0], hq, k.shape[1],
+         dim, DTYPES.get(dt, -1), _i(n, cu_q, dev, 1), _i(n, cu_k, dev, 1), R, scale, _r(n, out, dev, dt, dim),
+         _lse(n, lse, q, dev), _i(n, err, dev, 1))
 
 
 def lora_set_option(key: int, value: int) -> None:

@@ -7,7 +7,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "lora.h"
+#include <atomic>
+
+#include "lora_internal.cuh"
 
 namespace lora {
 
@@ -28,6 +30,15 @@ struct Rows {
     void *p;
     long long ts, hs;   // strides in elements
 };
+
+// Dynamic shared memory of a kernel, asked for once per device (bit d of `done`: device d has it).
+template <class K>
+inline int allow_smem(K kernel, size_t bytes, std::atomic<uint64_t> &done, int dev) {
+    if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return LORA_OK;
+    if (int rc = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes))) return rc;
+    if (dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return LORA_OK;
+}
 
 struct LayoutArgs {
     const int32_t *past, *fresh_len, *req_ids;

@@ -55,7 +55,7 @@ constexpr int kStages = 3;
 constexpr int kFixed = 2;                          // units that starting and joining a segment costs beside its rounds
 constexpr float kJump = 10.f;                      // log2 by which a score may exceed the reference
 constexpr int kShift = 5;                          // weights are scaled by 2^kShift in fp16
-constexpr int kJoinGroups = 4;                     // thread groups of the joining kernel
+constexpr int kJoinThreads = 512;
 
 // What a CTA leaves for the joining kernel about the segment that begins in it and ends in CTA `last`.
 struct Split {
@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_attend_kernel(AttendArgs a, Sp
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int G = a.hq / a.c.heads;
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining launch waits for this one's end by itself
     // Units of the batch and this CTA's range of them.
     const int per = (a.R + kThreads - 1) / kThreads, ra = min(a.R, tid * per), rb = min(a.R, ra + per);
     long long mine = 0;
@@ -708,58 +709,67 @@ __global__ void __launch_bounds__(kThreads, 3) kv_attend_kernel(AttendArgs a, Sp
     cp_wait<0>();
 }
 
-// Joins the pieces of the segment that begins in CTA blockIdx.x, in order.
+// Joins the pieces of the segment that begins in CTA blockIdx.x, in order: a warp (two with 8 columns) per column, its
+// lanes DIM / 32 dimensions each.
 template <int DIM, int NT, bool BF>
-__global__ void __launch_bounds__(kThreads * kJoinGroups) kv_join_kernel(AttendArgs a, const Split *split, const float *part) {
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, const Split *split, const float *part) {
     using H = typename std::conditional<BF, __nv_bfloat16, __half>::type;
-    constexpr int NC = 8 * NT, kChunks = DIM / 8;
-    __shared__ float sx[kJoinGroups][8][DIM], sl[kJoinGroups][8];
+    constexpr int NC = 8 * NT, E = DIM / 32, W = kJoinThreads / 32 / NC;   // W: warps of a column
+    __shared__ float sm_o[W][NC][DIM], sm_l[W][NC];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Split s = split[blockIdx.x];
     if (s.last == 0) return;
     const int G = a.hq / a.c.heads, first = blockIdx.x, n = s.last - first + 1;
-    const int grp = threadIdx.x / kThreads, tid = threadIdx.x % kThreads;
-    const int q0 = a.cu_q[s.r], nq = a.cu_q[s.r + 1] - q0;
+    const int lane = threadIdx.x & 31, col = (threadIdx.x >> 5) % NC, w = (threadIdx.x >> 5) / NC;
+    const int q0 = a.cu_q[s.r], nq = a.cu_q[s.r + 1] - q0, gc = s.ct * NC + col;
+    if (W == 1 && gc >= nq * G) return;
     // piece i: the second slot of the first CTA, the first slot of the others
     const auto at = [&](int i) { return part + (size_t)(2 * (first + i) + (i == 0)) * partial_floats(DIM, NC); };
-    for (int nt = 0; nt < NT; ++nt) {
-        __syncthreads();
-        // kChunks = 16 (8): 128 threads are 8 (16, half of them idle) columns
-        const int col = tid / kChunks, d0 = (tid % kChunks) * 8, cc = nt * 8 + col;
-        float x[8] = {}, ll = 0.f, mm = -INFINITY;
-        if (col < 8) {
-            for (int i = 0; i < n; ++i) mm = fmaxf(mm, at(i)[NC * DIM + cc]);
-            const float ref = mm == -INFINITY ? 0.f : mm;
-            for (int i = grp; i < n; i += kJoinGroups) {
-                const float *p = at(i);
-                const float f = ex2(p[NC * DIM + cc] - ref);
-                ll = fmaf(f, p[NC * DIM + NC + cc], ll);
-                const float4 u = *reinterpret_cast<const float4 *>(p + cc * DIM + d0), v = *reinterpret_cast<const float4 *>(p + cc * DIM + d0 + 4);
-                x[0] = fmaf(f, u.x, x[0]); x[1] = fmaf(f, u.y, x[1]); x[2] = fmaf(f, u.z, x[2]); x[3] = fmaf(f, u.w, x[3]);
-                x[4] = fmaf(f, v.x, x[4]); x[5] = fmaf(f, v.y, x[5]); x[6] = fmaf(f, v.z, x[6]); x[7] = fmaf(f, v.w, x[7]);
-            }
-            for (int k = 0; k < 8; ++k) sx[grp][col][d0 + k] = x[k];
-            if (d0 == 0) sl[grp][col] = ll;
+    float mm = -INFINITY;
+    for (int i = lane; i < n; i += 32) mm = fmaxf(mm, at(i)[NC * DIM + col]);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, d));
+    const float ref = mm == -INFINITY ? 0.f : mm;
+    float x[E] = {}, ll = 0.f;
+#pragma unroll 8
+    for (int i = w; i < n; i += W) {
+        const float *p = at(i);
+        const float f = ex2(p[NC * DIM + col] - ref);
+        ll = fmaf(f, p[NC * DIM + NC + col], ll);
+        if (E == 4) {
+            const float4 u = *reinterpret_cast<const float4 *>(p + col * DIM + lane * 4);
+            x[0] = fmaf(f, u.x, x[0]);
+            x[1] = fmaf(f, u.y, x[1]);
+            x[E - 2] = fmaf(f, u.z, x[E - 2]);
+            x[E - 1] = fmaf(f, u.w, x[E - 1]);
+        } else {
+            const float2 u = *reinterpret_cast<const float2 *>(p + col * DIM + lane * 2);
+            x[0] = fmaf(f, u.x, x[0]);
+            x[1] = fmaf(f, u.y, x[1]);
         }
-        __syncthreads();
-        const int gc = s.ct * NC + cc;
-        if (grp != 0 || col >= 8 || gc >= nq * G) continue;
-        ll = 0.f;
-        for (int j = 0; j < kJoinGroups; ++j) ll += sl[j][col];
-        const int qi = gc / G, head = s.h * G + gc - qi * G;
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        uint4 u;
-        H *e = reinterpret_cast<H *>(&u);
-        for (int k = 0; k < 8; ++k) {
-            float y = 0.f;
-            for (int j = 0; j < kJoinGroups; ++j) y += sx[j][col][d0 + k];
-            e[k] = (H)(y * inv);
-        }
-        *reinterpret_cast<uint4 *>(reinterpret_cast<H *>(a.o.p) + (long long)(q0 + qi) * a.o.ts + (long long)head * a.o.hs + d0) = u;
-        if (a.lse && d0 == 0)
-            a.lse[(size_t)(q0 + qi) * a.hq + head] =
-                ll == 0.f ? -INFINITY : 0.6931471805599453f * ((mm == -INFINITY ? 0.f : mm) + log2f(ll));
     }
+    if (W > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sm_o[w][col][lane * E + e] = x[e];
+        if (lane == 0) sm_l[w][col] = ll;
+        __syncthreads();
+        if (w != 0 || gc >= nq * G) return;
+#pragma unroll
+        for (int k = 1; k < W; ++k) {
+            ll += sm_l[k][col];
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] += sm_o[k][col][lane * E + e];
+        }
+    }
+    const int qi = gc / G, head = s.h * G + gc - qi * G;
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    H *out = reinterpret_cast<H *>(a.o.p) + (long long)(q0 + qi) * a.o.ts + (long long)head * a.o.hs + lane * E;
+    alignas(8) H y[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = (H)(x[e] * inv);
+    if (E == 4) *reinterpret_cast<uint2 *>(out) = *reinterpret_cast<const uint2 *>(y);
+    else *reinterpret_cast<uint32_t *>(out) = *reinterpret_cast<const uint32_t *>(y);
+    if (a.lse && lane == 0) a.lse[(size_t)(q0 + qi) * a.hq + head] = ll == 0.f ? -INFINITY : 0.6931471805599453f * (ref + log2f(ll));
 }
 
 int tiles_of(int hq, int hkv, int max_q) { return (long long)max_q * (hq / hkv) <= 8 ? 1 : 2; }
@@ -774,15 +784,17 @@ int launch(const AttendArgs &a, cudaStream_t st) {
     float *part = reinterpret_cast<float *>(static_cast<char *>(a.ws) + kSplitBytes);
     constexpr int U = granules_at_once<NT>();
     const size_t smem = sizeof(Smem<DIM, NT, U>);
-    if (int rc = cuda_check(cudaFuncSetAttribute(kv_attend_kernel<DIM, NT, U, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
-        return rc;
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (int rc = cuda_check(cudaGetDevice(&dev))) return rc;
+    if (int rc = allow_smem(kv_attend_kernel<DIM, NT, U, BF>, smem, done, dev)) return rc;
     const int grid = kMaxCtas;
     kv_attend_kernel<DIM, NT, U, BF><<<grid, kThreads, smem, st>>>(a, split, part);
     count_launch();
     if (int rc = cuda_check(cudaGetLastError())) return rc;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads * kJoinGroups);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -626,13 +626,16 @@ int launch(const PromptArgs &a, cudaStream_t st) {
     if (int rc = rows_map(&maps.v, vr, DIM, a.hkv, a.Tk, a.dtype, 1, kN)) return rc;
     const size_t smem = sizeof(Smem<DIM>) + 1024;
     static_assert(sizeof(Smem<DIM>) + 1024 <= 227 * 1024, "prompt kernel: shared memory beyond the per-block limit");
-    if (int rc = cuda_check(cudaFuncSetAttribute(prompt_kernel<DIM, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))) return rc;
+    static std::atomic<uint64_t> done{0};
     static_assert(kThreads * 168 == 128 * (88 + 2 * 208), "register split");
-    cudaFuncAttributes fa;
-    if (int rc = cuda_check(cudaFuncGetAttributes(&fa, prompt_kernel<DIM, BF>))) return rc;
-    if (fa.numRegs != 168) return LORA_ERR_CUDA;   // the row owners would wait for registers that the block does not have
     int dev = 0, sms = 0;
     if (int rc = cuda_check(cudaGetDevice(&dev))) return rc;
+    if (dev >= 64 || !(done.load() >> dev & 1)) {
+        cudaFuncAttributes fa;
+        if (int rc = cuda_check(cudaFuncGetAttributes(&fa, prompt_kernel<DIM, BF>))) return rc;
+        if (fa.numRegs != 168) return LORA_ERR_CUDA;   // the row owners would wait for registers that the block does not have
+    }
+    if (int rc = allow_smem(prompt_kernel<DIM, BF>, smem, done, dev)) return rc;
     if (int rc = cuda_check(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev))) return rc;
     prompt_kernel<DIM, BF><<<(int)(items < sms ? items : sms), kThreads, smem, st>>>(maps, k);
     count_launch();
