@@ -15,11 +15,12 @@
 // operand is free as long as both sides use it, and so is the order of tokens:
 // a thread reads whole words of codes from shared memory and a mask-and-or
 // turns bit fields into numbers.
-//   K, bf16 queries: field | 0x4300 is the bf16 number 128 + n; the offset is
-//   taken out of the finished product with the row sums of q (scores keep
-//   about 2^-19 of sum |q| |k|, far below what bf16 queries carry).
-//   K, fp16 queries, and V: field | 0x6400 is the fp16 number 1024 + n (or
-//   1024 + 16 n for the odd fields); one fused multiply-add makes it n - 8.
+//   field | 0x6400 is the fp16 number 1024 + n, or 1024 + 16 n for the odd fields.
+//   K: queries meet odd fields divided by 16, and the accumulators start at minus
+//   (1032 sum of even + 72 sum of odd) query elements, so that they end at
+//   q . (n - 8).  The queries go in as fp16 numbers times a power of two of their
+//   own (exact down to 2^-24 of the row's largest element).
+//   V: one fused multiply-add makes it n - 8.
 // So the products take exact integers; steps and lows enter in fp32: a score is
 // step * (q . n) + low * sum q per group of 64 dimensions, the weight of a value
 // is p * step per group, and sum p * (low + 8 step) is kept apart.  p * step is
@@ -50,7 +51,7 @@ namespace lora {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kMaxCtas = 444;                      // 3 CTAs on each of 148 SMs
+constexpr int kMaxCtas = 444;                      // one column tile: 3 CTAs on each of 148 SMs; two: 2
 constexpr int kStages = 3;
 constexpr int kFixed = 2;                          // units that starting and joining a segment costs beside its rounds
 constexpr float kJump = 10.f;                      // log2 by which a score may exceed the reference
@@ -111,9 +112,9 @@ struct Walk {
         bool bad;
         q = load_req<NC, ROUND>(a, r, G, bad);
         const int all = q.rounds + kFixed;
-        const long long seg = off / all;
+        const long long seg = off <= UINT32_MAX ? (long long)((uint32_t)off / (uint32_t)all) : off / all;
         const int from = (int)(off - seg * all), to = (int)min((long long)all, from + units);
-        h = (int)(seg / q.tiles);
+        h = q.tiles == 1 ? (int)seg : (int)(seg / q.tiles);
         ct = (int)(seg - (long long)h * q.tiles);
         round = max(0, from - kFixed);
         n = max(0, to - kFixed) - round;
@@ -170,39 +171,26 @@ __device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t b, uint32_t c) {
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
     return y;
 }
-// d += a b on fp16 (BF = false) or bf16 operands, fp32 accumulators.
-template <bool BF>
+// d += a b, fp16 operands, fp32 accumulators; mma_from: d = a b + (c0, c1, c0, c1).
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    if (BF)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                     "{%0, %1, %2, %3};" : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                     "{%0, %1, %2, %3};" : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};" : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// d = a b
-template <bool BF>
-__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    if (BF)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                     "{%10, %10, %10, %10};" : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                     "{%10, %10, %10, %10};" : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                                         float c0, float c1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%10, %11, %10, %11};" : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 // The masks and exponents of the unpacking, in registers: a mask-and-or with
 // two literals would take two instructions.
 struct Consts {
-    uint32_t lo, hi, h1024, b128, sixteenth;
+    uint32_t lo, hi, h1024, sixteenth;
     __device__ __forceinline__ Consts() {
         asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(lo));
         asm volatile("mov.b32 %0, 0x00f000f0;" : "=r"(hi));
         asm volatile("mov.b32 %0, 0x64006400;" : "=r"(h1024));
-        asm volatile("mov.b32 %0, 0x43004300;" : "=r"(b128));
         asm volatile("mov.b32 %0, 0x2c002c00;" : "=r"(sixteenth));
     }
 };
@@ -224,10 +212,13 @@ __device__ __forceinline__ void unpack_h(uint32_t w, uint32_t (&x)[4], const Con
     x[2] = add_h2(and_or(v, k.lo, k.h1024), sub);
     x[3] = fma_h2(and_or(v, k.hi, k.h1024), k.sixteenth, sub72);
 }
-// Four bf16 pairs 128 + n.
-__device__ __forceinline__ void unpack_b(uint32_t w, uint32_t (&x)[4], const Consts &k) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = and_or(w >> (4 * j), k.lo, k.b128);
+// Four fp16 pairs 1024 + n (even fields) and 1024 + 16 n (odd fields).
+__device__ __forceinline__ void unpack_raw(uint32_t w, uint32_t (&x)[4], const Consts &k) {
+    const uint32_t v = w >> 8;
+    x[0] = and_or(w, k.lo, k.h1024);
+    x[1] = and_or(w, k.hi, k.h1024);
+    x[2] = and_or(v, k.lo, k.h1024);
+    x[3] = and_or(v, k.hi, k.h1024);
 }
 // (step, low) of a token's groups.
 template <int NG>
@@ -242,7 +233,7 @@ __device__ __forceinline__ void load_params(const unsigned char *p, float2 (&x)[
 }
 
 template <int DIM, int NT, int U, bool BF>
-__global__ void __launch_bounds__(kThreads, 3) kv_attend_kernel(AttendArgs a, Split *split, float *part) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attend_kernel(AttendArgs a, Split *split, float *part) {
     using H = typename std::conditional<BF, __nv_bfloat16, __half>::type;
     constexpr int NC = 8 * NT, NG = DIM / LORA_KV_GROUP, GB = kv_granule_bytes(DIM), HB = kv_half_bytes(DIM), CB = kv_code_bytes(DIM);
     constexpr int ROUND = kWarps * U;
@@ -278,8 +269,12 @@ __global__ void __launch_bounds__(kThreads, 3) kv_attend_kernel(AttendArgs a, Sp
         total += sm.scan[w];
     }
     const long long ctas = min((long long)gridDim.x, total);
-    const long long u0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
-    const long long u1 = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : total;
+    const auto begin_of = [&](long long cta) {   // 32-bit division where it fits: it is on the way to the first load
+        const long long x = total * cta;
+        return x <= UINT32_MAX ? (long long)((uint32_t)x / (uint32_t)ctas) : x / ctas;
+    };
+    const long long u0 = blockIdx.x < ctas ? begin_of(blockIdx.x) : total;
+    const long long u1 = blockIdx.x < ctas ? begin_of(blockIdx.x + 1) : total;
     if (tid == 0) split[blockIdx.x].last = 0;
     if (u0 >= u1) return;
     if (run <= u0 && u0 < run + mine) {
@@ -299,26 +294,40 @@ __global__ void __launch_bounds__(kThreads, 3) kv_attend_kernel(AttendArgs a, Sp
     comp.start(a, G, sm.first, u0 - sm.base, u1 - u0);
     if (comp.n == 0 && !comp.next(a, G)) return;
     load = comp;
+    // Queries of a piece, asked for before they are needed: behind the prologue's table and cache loads, or the join.
+    uint4 raw[NT][NG][2];
+    const auto load_queries = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int gc = comp.ct * NC + nt * 8 + g, qi = gc / G, head = comp.h * G + gc - qi * G;
+            const H *row = reinterpret_cast<const H *>(a.q.p) + (long long)(comp.q.q0 + qi) * a.q.ts + (long long)head * a.q.hs;
+#pragma unroll
+            for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    raw[nt][ng][i] = make_uint4(0, 0, 0, 0);
+                    if (gc < comp.q.nq * G) raw[nt][ng][i] = *reinterpret_cast<const uint4 *>(row + 64 * ng + 16 * t4 + 8 * i);
+                }
+        }
+    };
+    load_queries();
 
     // The warp's granules, U at a time, into its ring.
     const Consts kc;
     const uint32_t ring = ptx::smem_u32(sm.ring[warp]) + lane * 16;
     const unsigned char *pages = a.c.pages + lane * 16;
     int lg = load.g0() + U * warp, lend = load.g1(), in_ids = 0;
-    long long where = -1;   // lane i: byte offset of the i-th granule the warp loads from the last fetch on, -1: none
+    int page_of = -1, at_of = 0;   // lane i: page and byte offset in it of the i-th granule the warp loads from the last fetch on
     bool more = true;
     uint32_t valid = 0;     // bits s U .. s U + U - 1: the granules that stage s holds
     int in_slot = 0;
     const auto fetch_ids = [&]() {   // the warp's next 32 granules of the piece
         in_ids = 0;
         const int gi = lg + ROUND * (lane / U) + lane % U, blk = gi / a.c.granules;
-        where = -1;
+        at_of = -1;   // none
         if (gi < lend) {
-            const int page = a.table[(size_t)load.r * a.max_blocks + blk];
-            if (page >= 0 && page < a.c.num_pages)
-                where = page * a.c.page_bytes + (long long)(load.h * a.c.granules + gi - blk * a.c.granules) * GB;
-            else if (a.err)
-                atomicOr(a.err, LORA_DEV_ERR_BAD_PAGE);
+            at_of = (load.h * a.c.granules + gi - blk * a.c.granules) * GB;
+            page_of = a.table[(size_t)load.r * a.max_blocks + blk];   // looked at when the granule is asked for: nothing waits here
         }
     };
     const auto advance = [&]() {
@@ -336,14 +345,17 @@ __global__ void __launch_bounds__(kThreads, 3) kv_attend_kernel(AttendArgs a, Sp
             uint32_t bits = 0;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const long long off = __shfl_sync(~0u, where, in_ids + u);
-                if (off >= 0) {
-                    const unsigned char *src = pages + off;
+                const int page = __shfl_sync(~0u, page_of, in_ids + u), at = __shfl_sync(~0u, at_of, in_ids + u);
+                if (at < 0) continue;
+                if (page >= 0 && page < a.c.num_pages) {
+                    const unsigned char *src = pages + page * a.c.page_bytes + at;
                     const uint32_t dst = ring + (in_slot * U + u) * GB;
 #pragma unroll
                     for (int i = 0; i < GB / 512; ++i) cp16(dst + 512 * i, src + 512 * i);
                     if (lane < GB % 512 / 16) cp16(dst + GB / 512 * 512, src + GB / 512 * 512);
                     bits |= 1u << u;
+                } else if (lane == 0 && a.err) {
+                    atomicOr(a.err, LORA_DEV_ERR_BAD_PAGE);
                 }
             }
             valid = (valid & ~(((1u << U) - 1) << (in_slot * U))) | bits << (in_slot * U);
@@ -360,44 +372,73 @@ __global__ void __launch_bounds__(kThreads, 3) kv_attend_kernel(AttendArgs a, Sp
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue();
 
-    // Scores stay as step * (q . n) + ... until the exponential, which takes them times c (>= 0: a negative scale
-    // turns the queries' signs).
-    const float c = fabsf(a.scale) * 1.4426950408889634f, jump = kJump / c;
-    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+    // Scores stay as step * (q . (n - 8)) + ... until the exponential, which takes them times cq = c 2^qx (c >= 0: a negative
+    // scale turns the queries' signs).
+    const float c = fabsf(a.scale) * 1.4426950408889634f;
     const int tok = g ^ ((g >> 1) & 1);   // token (of 8) in the operands' row g: both tokens of a pair on different banks
     int out_slot = 0;
     bool first_piece = true;
     for (;;) {
-        // Queries of this piece: fragments, and per group their sums.
+        // Queries of this piece as fp16 numbers times 2^-qx: fragments, per group their sums and the accumulators' start.
         uint32_t qf[NT][NG][4][2];
-        float qs[NT][NG][2];
+        float qs[NT][NG][2], start[NT][NG][2], cq[NT][2], jump[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int gc = comp.ct * NC + nt * 8 + g;
-            const bool ok = gc < comp.q.nq * G;
-            const int qi = gc / G, head = comp.h * G + gc - qi * G;
-            const H *row = reinterpret_cast<const H *>(a.q.p) + (long long)(comp.q.q0 + qi) * a.q.ts + (long long)head * a.q.hs;
+            float scale = 1.f;   // 2^-qx
+            {
+                float top = 0.f;
+#pragma unroll
+                for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf((float)reinterpret_cast<const H *>(&raw[nt][ng][i])[j]));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                // the largest element goes to [2^13, 2^14): odd ones are divided by 16, sums of products stay far from fp32's ends
+                const uint32_t e = __float_as_uint(top) >> 23;
+                if (e != 0 && e != 255) scale = __uint_as_float(min(267u - e, 254u) << 23);
+            }
 #pragma unroll
             for (int ng = 0; ng < NG; ++ng) {
-                float sum = 0.f;
+                float even = 0.f, odd = 0.f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    uint4 u = make_uint4(0, 0, 0, 0);
-                    if (ok) u = *reinterpret_cast<const uint4 *>(row + 64 * ng + 16 * t4 + 8 * i);
-                    u.x ^= flip; u.y ^= flip; u.z ^= flip; u.w ^= flip;
-                    const H *e = reinterpret_cast<const H *>(&u);
+                    const H *e = reinterpret_cast<const H *>(&raw[nt][ng][i]);
+                    float x[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sum += (float)e[j];
+                    for (int j = 0; j < 8; ++j) {
+                        x[j] = (float)e[j] * scale;
+                        if (a.scale < 0.f) x[j] = -x[j];
+                        if (j & 1) {
+                            odd += x[j];
+                            x[j] *= 0.0625f;
+                        } else {
+                            even += x[j];
+                        }
+                    }
                     // pairs (j, j + 4) of the eight dimensions, as the codes unpack
-                    qf[nt][ng][2 * i][0] = __byte_perm(u.x, u.z, 0x5410);
-                    qf[nt][ng][2 * i][1] = __byte_perm(u.x, u.z, 0x7632);
-                    qf[nt][ng][2 * i + 1][0] = __byte_perm(u.y, u.w, 0x5410);
-                    qf[nt][ng][2 * i + 1][1] = __byte_perm(u.y, u.w, 0x7632);
+                    qf[nt][ng][2 * i][0] = pack_h2(x[0], x[4]);
+                    qf[nt][ng][2 * i][1] = pack_h2(x[1], x[5]);
+                    qf[nt][ng][2 * i + 1][0] = pack_h2(x[2], x[6]);
+                    qf[nt][ng][2 * i + 1][1] = pack_h2(x[3], x[7]);
                 }
-                sum += __shfl_xor_sync(~0u, sum, 1);
-                sum += __shfl_xor_sync(~0u, sum, 2);
-                qs[nt][ng][0] = __shfl_sync(~0u, sum, 8 * t4);
-                qs[nt][ng][1] = __shfl_sync(~0u, sum, 8 * t4 + 4);
+#pragma unroll
+                for (int d = 1; d < 4; d <<= 1) {
+                    even += __shfl_xor_sync(~0u, even, d);
+                    odd += __shfl_xor_sync(~0u, odd, d);
+                }
+                const float from = fmaf(-1032.f, even, -72.f * odd);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    qs[nt][ng][e] = __shfl_sync(~0u, even + odd, 8 * t4 + 4 * e);
+                    start[nt][ng][e] = __shfl_sync(~0u, from, 8 * t4 + 4 * e);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                cq[nt][e] = c / __shfl_sync(~0u, scale, 8 * t4 + 4 * e);
+                jump[nt][e] = kJump / cq[nt][e];
             }
         }
         // Last key each of the thread's columns sees, and the least of the tile.
@@ -435,19 +476,16 @@ __global__ void __launch_bounds__(kThreads, 3) kv_attend_kernel(AttendArgs a, Sp
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         uint32_t x[4], y[4];
-                        if (BF) {
-                            unpack_b(i ? w0.y : w0.x, x, kc);
-                            unpack_b(i ? w1.y : w1.x, y, kc);
-                        } else {
-                            unpack_h(i ? w0.y : w0.x, x, kc);
-                            unpack_h(i ? w1.y : w1.x, y, kc);
-                        }
+                        unpack_raw(i ? w0.y : w0.x, x, kc);
+                        unpack_raw(i ? w1.y : w1.x, y, kc);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             // fields (0, 4) and (1, 5) against dimensions 0, 4 and 1, 5; then (2, 6) and (3, 7)
-                            if (i == 0) mma_first<BF>(acc[nt][ng], x[0], y[0], x[1], y[1], qf[nt][ng][0][0], qf[nt][ng][0][1]);
-                            else mma<BF>(acc[nt][ng], x[0], y[0], x[1], y[1], qf[nt][ng][2][0], qf[nt][ng][2][1]);
-                            mma<BF>(acc[nt][ng], x[2], y[2], x[3], y[3], qf[nt][ng][2 * i + 1][0], qf[nt][ng][2 * i + 1][1]);
+                            if (i == 0)
+                                mma_from(acc[nt][ng], x[0], y[0], x[1], y[1], qf[nt][ng][0][0], qf[nt][ng][0][1], start[nt][ng][0], start[nt][ng][1]);
+                            else
+                                mma(acc[nt][ng], x[0], y[0], x[1], y[1], qf[nt][ng][2][0], qf[nt][ng][2][1]);
+                            mma(acc[nt][ng], x[2], y[2], x[3], y[3], qf[nt][ng][2 * i + 1][0], qf[nt][ng][2 * i + 1][1]);
                         }
                     }
                 }
@@ -457,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_attend_kernel(AttendArgs a, Sp
                     load_params<NG>(k + CB + (tok + 8 * w) * 4 * NG, p);
 #pragma unroll
                     for (int ng = 0; ng < NG; ++ng) {
-                        const float low = fmaf(BF ? -128.f : 8.f, p[ng].x, p[ng].y);
+                        const float low = fmaf(8.f, p[ng].x, p[ng].y);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -534,10 +572,10 @@ __global__ void __launch_bounds__(kThreads, 3) kv_attend_kernel(AttendArgs a, Sp
                         t = fmaxf(t, __shfl_xor_sync(~0u, t, 8));
                         t = fmaxf(t, __shfl_xor_sync(~0u, t, 16));
                         const float n = fmaxf(m[nt][e], t);
-                        const float f = m[nt][e] == n ? 1.f : m[nt][e] == -INFINITY ? 0.f : ex2((m[nt][e] - n) * c);
+                        const float f = m[nt][e] == n ? 1.f : m[nt][e] == -INFINITY ? 0.f : ex2((m[nt][e] - n) * cq[nt][e]);
                         m[nt][e] = n;
-                        mc[nt][e] = n == -INFINITY ? 0.f : n * c;
-                        thr[nt][e] = n + jump;
+                        mc[nt][e] = n == -INFINITY ? 0.f : n * cq[nt][e];
+                        thr[nt][e] = n + jump[nt][e];
                         l[nt][e] *= f;
 #pragma unroll
                         for (int ng = 0; ng < NG; ++ng) {
@@ -559,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_attend_kernel(AttendArgs a, Sp
                     float p[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        p[e] = ex2(fmaf(s[u][nt][e], c, -mc[nt][e & 1]));
+                        p[e] = ex2(fmaf(s[u][nt][e], cq[nt][e & 1], -mc[nt][e & 1]));
                         if (EDGE && s[u][nt][e] == -INFINITY) p[e] = 0.f;   // with scale 0 too
                         l[nt][e & 1] += p[e];
                     }
@@ -598,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_attend_kernel(AttendArgs a, Sp
                         const int i = 2 * (mt & 1);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            mma<false>(o[nt][ng][mt], z[0][i], z[0][i + 1], z[1][i], z[1][i + 1], pb[nt][ng][0], pb[nt][ng][1]);
+                            mma(o[nt][ng][mt], z[0][i], z[0][i + 1], z[1][i], z[1][i + 1], pb[nt][ng][0], pb[nt][ng][1]);
                     }
                 }
             }
@@ -616,6 +654,9 @@ __global__ void __launch_bounds__(kThreads, 3) kv_attend_kernel(AttendArgs a, Sp
             else if (bits) step(std::true_type{}, st, gi, bits);
         }
 
+        const Walk<NC, ROUND> cur = comp;
+        const bool again = comp.next(a, G);
+        if (again) load_queries();
         // Join the warps.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -653,8 +694,8 @@ __global__ void __launch_bounds__(kThreads, 3) kv_attend_kernel(AttendArgs a, Sp
                 }
             }
         __syncthreads();
-        const bool whole = comp.round == 0 && comp.n == comp.q.rounds;
-        const int slot = 2 * blockIdx.x + (first_piece && comp.round > 0 ? 0 : 1);
+        const bool whole = cur.round == 0 && cur.n == cur.q.rounds;
+        const int slot = 2 * blockIdx.x + (first_piece && cur.round > 0 ? 0 : 1);
         float *dst = part + (size_t)slot * partial_floats(DIM, NC);
         constexpr int kChunks = DIM / 8;
         for (int i = tid; i < NC * kChunks; i += kThreads) {
@@ -682,29 +723,29 @@ __global__ void __launch_bounds__(kThreads, 3) kv_attend_kernel(AttendArgs a, Sp
                 }
                 continue;
             }
-            const int gc = comp.ct * NC + col;
-            if (gc >= comp.q.nq * G) continue;
-            const int qi = gc / G, head = comp.h * G + gc - qi * G;
+            const int gc = cur.ct * NC + col;
+            if (gc >= cur.q.nq * G) continue;
+            const int qi = gc / G, head = cur.h * G + gc - qi * G;
             const float inv = ll == 0.f ? 0.f : 1.f / ll;
             uint4 u;
             H *e = reinterpret_cast<H *>(&u);
 #pragma unroll
             for (int k = 0; k < 8; ++k) e[k] = (H)(x[k] * inv);
-            *reinterpret_cast<uint4 *>(reinterpret_cast<H *>(a.o.p) + (long long)(comp.q.q0 + qi) * a.o.ts +
+            *reinterpret_cast<uint4 *>(reinterpret_cast<H *>(a.o.p) + (long long)(cur.q.q0 + qi) * a.o.ts +
                                        (long long)head * a.o.hs + d0) = u;
             if (a.lse && d0 == 0)
-                a.lse[(size_t)(comp.q.q0 + qi) * a.hq + head] = ll == 0.f ? -INFINITY : 0.6931471805599453f * (ref + log2f(ll));
+                a.lse[(size_t)(cur.q.q0 + qi) * a.hq + head] = ll == 0.f ? -INFINITY : 0.6931471805599453f * (ref + log2f(ll));
         }
-        if (tid == 0 && !whole && comp.round + comp.n < comp.q.rounds && !(first_piece && comp.round > 0)) {
+        if (tid == 0 && !whole && cur.round + cur.n < cur.q.rounds && !(first_piece && cur.round > 0)) {
             // the segment begins here and goes on: its last unit is u1 - 1 + (rounds not done)
-            const long long end = u1 - 1 + (comp.q.rounds - comp.round - comp.n);
+            const long long end = u1 - 1 + (cur.q.rounds - cur.round - cur.n);
             long long last = ((end + 1) * ctas + total - 1) / total - 1;   // the CTA whose range holds `end`
             while (total * (last + 1) / ctas <= end) ++last;
             while (total * last / ctas > end) --last;
-            split[blockIdx.x] = Split{comp.r, comp.h, comp.ct, (int)last};
+            split[blockIdx.x] = Split{cur.r, cur.h, cur.ct, (int)last};
         }
         first_piece = false;
-        if (!comp.next(a, G)) break;
+        if (!again) break;
     }
     cp_wait<0>();
 }
@@ -774,7 +815,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, con
 
 int tiles_of(int hq, int hkv, int max_q) { return (long long)max_q * (hq / hkv) <= 8 ? 1 : 2; }
 template <int NT>
-constexpr int granules_at_once() { return NT == 1 ? 2 : 1; }
+constexpr int ctas_per_sm() { return NT == 1 ? 3 : 2; }   // what the registers allow
 
 constexpr size_t kSplitBytes = (kMaxCtas * sizeof(Split) + 255) / 256 * 256;
 
@@ -782,13 +823,13 @@ template <int DIM, int NT, bool BF>
 int launch(const AttendArgs &a, cudaStream_t st) {
     Split *split = static_cast<Split *>(a.ws);
     float *part = reinterpret_cast<float *>(static_cast<char *>(a.ws) + kSplitBytes);
-    constexpr int U = granules_at_once<NT>();
+    constexpr int U = 2;
     const size_t smem = sizeof(Smem<DIM, NT, U>);
     static std::atomic<uint64_t> done{0};
     int dev = 0;
     if (int rc = cuda_check(cudaGetDevice(&dev))) return rc;
     if (int rc = allow_smem(kv_attend_kernel<DIM, NT, U, BF>, smem, done, dev)) return rc;
-    const int grid = kMaxCtas;
+    const int grid = 148 * ctas_per_sm<NT>();
     kv_attend_kernel<DIM, NT, U, BF><<<grid, kThreads, smem, st>>>(a, split, part);
     count_launch();
     if (int rc = cuda_check(cudaGetLastError())) return rc;
