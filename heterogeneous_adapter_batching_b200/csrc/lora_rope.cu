@@ -12,9 +12,10 @@
 //
 // Quantisation of 64 dimensions x of one head: low = fp16(min x), step =
 // fp16((max x - min x) / 15), code = clamp(round_even((x - low) / step), 0, 15).
-// The quotient is formed in 32 bits; where it lies within 2^-10 of a border
-// between two codes (its error is below 15.5 * 2^-21) the side is decided by the
-// sign of (x - low) - step * (border) in 64 bits, which is exact.
+// The quotient is formed in 32 bits; where it lies within 2^-17 of a border
+// between two codes (its error is below 15.5 * 3 * 2^-24) the side is decided by
+// the sign of (x - low) - step * (border) in 64 bits, which is exact.  That
+// happens to one warp in a hundred.
 //
 // Layout of the work: a head is dim / 16 chunks of 16 elements, one thread per
 // chunk: elements [8 c, 8 c + 8) and [rot / 2 + 8 c, + 8) in the half layout,
@@ -28,25 +29,30 @@
 namespace lora {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTok = 4;       // most tokens of one CTA
+constexpr int kThreads = 128;
+constexpr int kMaxTok = 2;       // most tokens of one CTA
 
+// Eight elements of a row as they lie in memory, and as numbers.
 template <class T> struct Elem;
 template <> struct Elem<float> {
-    static __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
-        const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    struct Raw { float4 a, b; };
+    static __device__ __forceinline__ Raw load(const float *p) {
+        return Raw{*reinterpret_cast<const float4 *>(p), *reinterpret_cast<const float4 *>(p + 4)};
+    }
+    static __device__ __forceinline__ void get(const Raw &r, float (&x)[8]) {
+        x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
+        x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
     }
     static __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
         *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
         *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
     }
 };
-template <class H, class H2>
+template <class H>
 struct Elem16 {
-    static __device__ __forceinline__ void load8(const H *p, float (&x)[8]) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    typedef uint4 Raw;
+    static __device__ __forceinline__ Raw load(const H *p) { return *reinterpret_cast<const uint4 *>(p); }
+    static __device__ __forceinline__ void get(const Raw &u, float (&x)[8]) {
         const H *h = reinterpret_cast<const H *>(&u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = (float)h[i];
@@ -59,36 +65,77 @@ struct Elem16 {
         *reinterpret_cast<uint4 *>(p) = u;
     }
 };
-template <> struct Elem<__nv_bfloat16> : Elem16<__nv_bfloat16, __nv_bfloat162> {};
-template <> struct Elem<__half> : Elem16<__half, __half2> {};
+template <> struct Elem<__nv_bfloat16> : Elem16<__nv_bfloat16> {};
+template <> struct Elem<__half> : Elem16<__half> {};
 
-__device__ __forceinline__ float min_nan(float a, float b) {
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-// Code of x for (step, low), inv = 1 / step (see the head of the file).
-__device__ __forceinline__ uint32_t code_of(float x, float low, float step, float inv) {
-    const float t = (x - low) * inv;
-    const float k = floorf(t);
-    float n = rintf(t);
-    if (fabsf(t - k - 0.5f) < 0x1p-10f) {
-        const double side = fma(-(double)step, (double)k + 0.5, (double)x - (double)low);
-        n = k + (side > 0.0 || (side == 0.0 && ((int)k & 1)) ? 1.f : 0.f);
+// Pairs of the row type: packing, unpacking, and the smaller of each (a NaN wins).
+template <class D> struct Pair;
+template <> struct Pair<__nv_bfloat16> {
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&p);
     }
-    return (uint32_t)fminf(fmaxf(n, 0.f), 15.f);   // a NaN becomes 0
+    static __device__ __forceinline__ float2 get(uint32_t u) {
+        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    }
+    static __device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b) {
+        uint32_t y;
+        asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+        return y;
+    }
+    static constexpr uint32_t kInf = 0x7f807f80u;
+};
+template <> struct Pair<__half> {
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const __half2 p = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&p);
+    }
+    static __device__ __forceinline__ float2 get(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2 *>(&u)); }
+    static __device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b) {
+        uint32_t y;
+        asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+        return y;
+    }
+    static constexpr uint32_t kInf = 0x7c007c00u;
+};
+// (least, minus the greatest) of eight packed elements.
+template <class D>
+__device__ __forceinline__ uint32_t range_of(const uint32_t (&u)[4]) {
+    uint32_t l = Pair<D>::less(Pair<D>::less(u[0], u[1]), Pair<D>::less(u[2], u[3]));
+    uint32_t g = Pair<D>::less(Pair<D>::less(u[0] ^ 0x80008000u, u[1] ^ 0x80008000u),
+                               Pair<D>::less(u[2] ^ 0x80008000u, u[3] ^ 0x80008000u));
+    return Pair<D>::less(__byte_perm(l, g, 0x5410), __byte_perm(l, g, 0x7632));
 }
 
-__device__ __forceinline__ uint32_t pack8(const float (&x)[8], float low, float step, float inv) {
+// Codes of eight elements for (step, low), inv = 1 / step or 0 (see the head of the file).
+template <class D>
+__device__ __forceinline__ uint32_t codes_of(const uint32_t (&u)[4], float low, float step, float inv) {
     uint32_t w = 0;
+    bool close = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w |= code_of(x[i], low, step, inv) << (4 * i);
+    for (int i = 3; i >= 0; --i) {
+        const float2 v = Pair<D>::get(u[i]);
+#pragma unroll
+        for (int k = 1; k >= 0; --k) {
+            const float t = fminf(fmaxf(((k ? v.y : v.x) - low) * inv, 0.f), 15.f);   // a NaN becomes 0
+            const float r = t + 12582912.f;                                           // 1.5 * 2^23: the nearest integer in the low bits
+            close |= fabsf(t - (r - 12582912.f)) > 0.5f - 0x1p-17f;
+            w = (w << 4) | (__float_as_uint(r) & 15u);
+        }
+    }
+    if (close) {   // some element lies at a border between codes: decide it exactly
+        w = 0;
+        for (int i = 7; i >= 0; --i) {
+            const float2 v = Pair<D>::get(u[0] * (i < 2) | u[1] * (i / 2 == 1) | u[2] * (i / 2 == 2) | u[3] * (i / 2 == 3));
+            const float x = i & 1 ? v.y : v.x, t = fminf(fmaxf((x - low) * inv, 0.f), 15.f), k = floorf(t);
+            float n = rintf(t);
+            if (fabsf(t - k - 0.5f) < 0x1p-16f) {
+                const double side = fma(-(double)step, (double)k + 0.5, (double)x - (double)low);
+                n = k + (side > 0.0 || (side == 0.0 && ((int)k & 1)) ? 1.f : 0.f);
+            }
+            w = (w << 4) | (uint32_t)n;
+        }
+    }
     return w;
 }
 
@@ -119,39 +166,70 @@ __device__ __forceinline__ void turn_interleaved(float (&x)[8], float (&y)[8], c
     }
 }
 
+// A walk over (token of the CTA, head) pairs, `step` heads at a time.
+struct HeadWalk {
+    int tl, head;
+    __device__ __forceinline__ void wrap(int heads) {
+        while (head >= heads) {
+            head -= heads;
+            ++tl;
+        }
+    }
+};
+
 template <class S, class D, bool CACHE>
 __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tok_per_cta) {
     // sine and cosine of the CTA's tokens, [token][pair], both precisions
     extern __shared__ double2 cs64[];
+    __shared__ int sm_pos[kMaxTok], sm_slot[kMaxTok];
     float2 *cs32 = reinterpret_cast<float2 *>(cs64 + (CACHE ? tok_per_cta * (a.rot / 2) : 0));
     const int half = a.rot / 2, t0 = blockIdx.x * tok_per_cta, nt = min(tok_per_cta, a.T - t0);
+    const int chunks = a.dim / 16, step = kThreads / chunks, heads = a.hq + a.hk + a.hv, c = threadIdx.x % chunks;
+    const bool split = 16 * c < a.rot && !a.interleaved;   // of a rotated head: the thread's elements are half a rotation apart
+    const int ds0 = split ? 8 * c : 16 * c, ds1 = split ? half + 8 * c : 16 * c + 8;
+
+    HeadWalk w{0, (int)threadIdx.x / chunks};
+    if (w.head >= step) w.tl = nt;                          // threads beyond the last whole head
+    w.wrap(heads);
+    typename Elem<S>::Raw r0, r1;
+    const auto load = [&]() {   // the walk's rows, one step ahead of their use
+        if (w.tl >= nt) return;
+        const bool q = w.head < a.hq, k = !q && w.head < a.hq + a.hk;
+        const Rows &src = q ? a.q : k ? a.k : a.v;
+        const int h = w.head - (q ? 0 : k ? a.hq : a.hq + a.hk);
+        const S *in = reinterpret_cast<const S *>(src.p) + (t0 + w.tl) * src.ts + h * src.hs;
+        r0 = Elem<S>::load(in + (q || k ? ds0 : 16 * c));
+        r1 = Elem<S>::load(in + (q || k ? ds1 : 16 * c + 8));
+    };
+    load();
+    if (threadIdx.x < nt) {
+        sm_pos[threadIdx.x] = a.positions[t0 + threadIdx.x];
+        if (CACHE) sm_slot[threadIdx.x] = a.slots[t0 + threadIdx.x];
+    }
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-        const int pos = a.positions[t0 + i / half];
-        double s, c;
-        sincos((double)pos * (double)a.freq[i % half], &s, &c);
+        const int tl = i / half, pos = a.positions[t0 + tl];
+        double s, co;
+        sincos((double)pos * (double)a.freq[i - tl * half], &s, &co);
         s *= a.mscale;
-        c *= a.mscale;
-        if (CACHE) cs64[i] = make_double2(c, s);
-        cs32[i] = make_float2((float)c, (float)s);
+        co *= a.mscale;
+        if (CACHE) cs64[i] = make_double2(co, s);
+        cs32[i] = make_float2((float)co, (float)s);
     }
     __syncthreads();
 
-    const int chunks = a.dim / 16, per_tok = (a.hq + a.hk + a.hv) * chunks;
-    for (int i = threadIdx.x; i < nt * per_tok; i += kThreads) {
-        const int tl = i / per_tok, t = t0 + tl, w = i - tl * per_tok;
-        const int head = w / chunks, c = w - head * chunks;
-        if (a.positions[t] < 0) continue;
+    while (w.tl < nt) {
+        const int tl = w.tl, t = t0 + tl, head = w.head;
+        float x[8], y[8];
+        Elem<S>::get(r0, x);
+        Elem<S>::get(r1, y);
+        w.head += step;
+        w.wrap(heads);
+        load();
+        if (sm_pos[tl] < 0) continue;
         const int kind = head < a.hq ? 0 : head < a.hq + a.hk ? 1 : 2;
         const int h = kind == 0 ? head : kind == 1 ? head - a.hq : head - a.hq - a.hk;
-        const Rows &src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-        const bool turned = kind < 2 && 16 * c < a.rot;
-        const bool split = turned && !a.interleaved;
-        const int d0 = split ? 8 * c : 16 * c, d1 = split ? half + 8 * c : 16 * c + 8;
-        const S *in = reinterpret_cast<const S *>(src.p) + t * src.ts + h * src.hs;
-        float x[8], y[8];
-        Elem<S>::load8(in + d0, x);
-        Elem<S>::load8(in + d1, y);
-        if (turned) {
+        const int d0 = kind < 2 ? ds0 : 16 * c, d1 = kind < 2 ? ds1 : 16 * c + 8;
+        if (kind < 2 && 16 * c < a.rot) {
             if (CACHE && kind == 1)
                 a.interleaved ? turn_interleaved<double>(x, y, cs64 + tl * half + 8 * c)
                               : turn_half<double>(x, y, cs64 + tl * half + 8 * c);
@@ -159,33 +237,27 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tok_per_
                 a.interleaved ? turn_interleaved<float>(x, y, cs32 + tl * half + 8 * c)
                               : turn_half<float>(x, y, cs32 + tl * half + 8 * c);
         }
+        uint32_t ux[4], uy[4];   // what the row type holds is what is written, and what is cached
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            ux[j] = Pair<D>::pack(x[2 * j], x[2 * j + 1]);
+            uy[j] = Pair<D>::pack(y[2 * j], y[2 * j + 1]);
+        }
         if (kind == 0 || (kind == 1 ? a.has_ko : a.has_vo)) {
             const Rows &dst = kind == 0 ? a.qo : kind == 1 ? a.ko : a.vo;
             D *out = reinterpret_cast<D *>(dst.p) + t * dst.ts + h * dst.hs;
-            Elem<D>::store8(out + d0, x);
-            Elem<D>::store8(out + d1, y);
+            *reinterpret_cast<uint4 *>(out + d0) = make_uint4(ux[0], ux[1], ux[2], ux[3]);
+            *reinterpret_cast<uint4 *>(out + d1) = make_uint4(uy[0], uy[1], uy[2], uy[3]);
         }
         if (!CACHE || kind == 0) continue;
-        const int slot = a.slots[t];
+        const int slot = sm_slot[tl];
         if (slot < 0) continue;
         const int page = slot / a.c.block, off = slot - page * a.c.block;
         if (page >= a.c.num_pages) {
             if (c == 0 && h == 0 && a.err) atomicOr(a.err, LORA_DEV_ERR_BAD_PAGE);
             continue;
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {   // what the row type holds is what is cached
-            x[j] = (float)(D)x[j];
-            y[j] = (float)(D)y[j];
-        }
-        float lo[2] = {x[0], y[0]}, hi[2] = {x[0], y[0]};
-#pragma unroll
-        for (int j = 1; j < 8; ++j) {
-            lo[0] = min_nan(lo[0], x[j]);
-            hi[0] = max_nan(hi[0], x[j]);
-            lo[1] = min_nan(lo[1], y[j]);
-            hi[1] = max_nan(hi[1], y[j]);
-        }
+        const uint32_t rx = range_of<D>(ux), ry = range_of<D>(uy);
         // the lanes of this head: chunks is 4 or 8 and heads start at multiples of it
         const int lane = threadIdx.x & 31;
         const uint32_t mask = (chunks == 8 ? 0xffu : 0xfu) << (lane & ~(chunks - 1));
@@ -193,20 +265,13 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tok_per_
         float step0 = 0.f, low0 = 0.f, step1 = 0.f, low1 = 0.f;
         unsigned char *base = half_of(a.c, a.dim, page, off, h, kind - 1);
         for (int g = 0; g < a.dim / LORA_KV_GROUP; ++g) {
-            float l = INFINITY, u = -INFINITY;
-            if (g0 == g) {
-                l = lo[0];
-                u = hi[0];
-            }
-            if (g1 == g) {
-                l = min_nan(l, lo[1]);
-                u = max_nan(u, hi[1]);
-            }
-            for (int d = 1; d < chunks; d <<= 1) {
-                l = min_nan(l, __shfl_xor_sync(mask, l, d));
-                u = max_nan(u, __shfl_xor_sync(mask, u, d));
-            }
-            const __half hl = __float2half_rn(l), hs = __float2half_rn((float)(((double)u - (double)l) / 15.0));
+            uint32_t r = Pair<D>::less(g0 == g ? rx : Pair<D>::kInf, g1 == g ? ry : Pair<D>::kInf);
+            for (int d = 1; d < chunks; d <<= 1) r = Pair<D>::less(r, __shfl_xor_sync(mask, r, d));
+            const float2 e = Pair<D>::get(r);   // least, minus the greatest
+            // the quotient by 15 rounded correctly: a first value, and its remainder times the reciprocal
+            const double diff = -(double)e.y - (double)e.x, first = diff * (1.0 / 15.0);
+            const double quot = fma(fma(-15.0, first, diff), 1.0 / 15.0, first);
+            const __half hl = __float2half_rn(e.x), hs = __float2half_rn((float)quot);
             if (c == 0)
                 reinterpret_cast<__half2 *>(base + kv_code_bytes(a.dim))[(off % LORA_KV_GRANULE) * (a.dim / LORA_KV_GROUP) + g] =
                     __halves2half2(hs, hl);
@@ -220,20 +285,18 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tok_per_
             }
         }
         unsigned char *row = base + (off % LORA_KV_GRANULE) * (a.dim / 2);
-        const uint32_t w0 = pack8(x, low0, step0, step0 > 0.f ? 1.f / step0 : 0.f);
-        const uint32_t w1 = pack8(y, low1, step1, step1 > 0.f ? 1.f / step1 : 0.f);
-        *reinterpret_cast<uint32_t *>(row + d0 / 2) = w0;
-        *reinterpret_cast<uint32_t *>(row + d1 / 2) = w1;
+        *reinterpret_cast<uint32_t *>(row + d0 / 2) = codes_of<D>(ux, low0, step0, step0 > 0.f ? 1.f / step0 : 0.f);
+        *reinterpret_cast<uint32_t *>(row + d1 / 2) = codes_of<D>(uy, low1, step1, step1 > 0.f ? 1.f / step1 : 0.f);
     }
 }
 
 template <class D>
-__global__ void __launch_bounds__(kThreads) kv_gather_kernel(GatherKvArgs a) {
-    const int chunks = a.dim / 16, per_tok = 2 * a.c.heads * chunks;
-    const long long n = (long long)a.T * per_tok;
-    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kThreads) {
-        const int t = (int)(i / per_tok), w = (int)(i - (long long)t * per_tok);
-        const int which = w / (a.c.heads * chunks), h = w / chunks - which * a.c.heads, c = w % chunks;
+__global__ void __launch_bounds__(kThreads) kv_gather_kernel(GatherKvArgs a, int tok_per_cta) {
+    const int chunks = a.dim / 16, step = kThreads / chunks, c = threadIdx.x % chunks, heads = 2 * a.c.heads;   // K heads, then V heads
+    const int t0 = blockIdx.x * tok_per_cta, nt = min(tok_per_cta, a.T - t0);
+    HeadWalk w{0, (int)threadIdx.x / chunks};
+    for (w.wrap(heads); w.tl < nt; w.head += step, w.wrap(heads)) {
+        const int t = t0 + w.tl, which = w.head >= a.c.heads, h = w.head - (which ? a.c.heads : 0);
         if (!(which ? a.has_v : a.has_k)) continue;
         const int slot = a.slots[t];
         if (slot < 0) continue;
@@ -261,8 +324,10 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(GatherKvArgs a) {
 
 template <class S, class D>
 int rope_types(const RopeArgs &a, cudaStream_t st) {
-    // few tokens: a CTA each, for latency; many: four share a CTA's angles
-    const int per = a.T >= 2368 ? kMaxTok : 1;
+    // A CTA per token for latency; from eight tokens per SM on two share one, whose threads then have twice the work behind one
+    // wait for the angles (with the cache, 32 + 8 + 8 heads of 128: 8.5 against 10.5 us at 256 tokens, 78 against 74 us at
+    // 8101; CTAs of 256 threads with four tokens take 81 us).
+    const int per = a.T >= 1184 ? kMaxTok : 1;
     const int grid = (a.T + per - 1) / per;
     const size_t pairs = (size_t)per * (a.rot / 2);
     if (a.slots)
@@ -282,11 +347,10 @@ int launch_rope(const RopeArgs &a, int src, int dst, cudaStream_t st) {
 }
 
 int launch_kv_gather(const GatherKvArgs &a, int dst, cudaStream_t st) {
-    const long long n = (long long)a.T * 2 * a.c.heads * (a.dim / 16);
-    const int grid = (int)min((n + kThreads - 1) / kThreads, 148LL * 32);
-    if (dst == LORA_BF16) kv_gather_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a);
-    else if (dst == LORA_FP16) kv_gather_kernel<__half><<<grid, kThreads, 0, st>>>(a);
-    else kv_gather_kernel<float><<<grid, kThreads, 0, st>>>(a);
+    const int per = a.T >= 1184 ? kMaxTok : 1, grid = (a.T + per - 1) / per;
+    if (dst == LORA_BF16) kv_gather_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, per);
+    else if (dst == LORA_FP16) kv_gather_kernel<__half><<<grid, kThreads, 0, st>>>(a, per);
+    else kv_gather_kernel<float><<<grid, kThreads, 0, st>>>(a, per);
     count_launch();
     return cuda_check(cudaGetLastError());
 }

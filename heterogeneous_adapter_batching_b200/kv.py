@@ -1,0 +1,122 @@
+"""KV cache of a served model in the pages of a lora_pool, and the metadata of a
+step (device tensors only; every computation goes through the C-ABI calls in
+_binding).
+
+Page "Multi-LoRA Serving in Production" (llms.blog), section "Unified Paging
+Architecture": KV-cache tensors and adapter weights share one pool of pages;
+page "LoRA Adapters at Serve Time with vLLM Multi-LoRA", section "The Inference
+Mechanism: A Worked Scenario": KV blocks are allocated per request, and every
+step batches requests with adapters of their own."""
+from __future__ import annotations
+
+import math
+from typing import Optional
+
+import torch
+
+from . import _binding as B
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[dict] = None):
+    """(inverse frequencies [rot_dim / 2] fp32 on the host, mscale) for lora_rope and lora_kv_append.
+
+    scaling: None, or {"kind": ..., "factor": s, ...} for contexts s times as long as the model was trained on:
+      "linear"   every position divided by s
+      "ntk"      base raised to base * s^(rot_dim / (rot_dim - 2)): the slowest pair slowed by s, the fastest not at all
+      "yarn"     pairs that turn fewer than beta_slow (1) times over original_max_position tokens slowed by s, those that
+                 turn more than beta_fast (32) times kept, a ramp in the pair index between; mscale = 0.1 ln s + 1
+      "bands"    pairs with wavelengths above original_max_position / low_freq_factor (1) slowed by s, below
+                 original_max_position / high_freq_factor (4) kept, interpolated in between
+    """
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim is a positive even number")
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
+    f = base ** (-i / rot_dim)
+    if scaling is None:
+        return f.float(), 1.0
+    kind, s = scaling["kind"], float(scaling["factor"])
+    if kind == "linear":
+        return (f / s).float(), 1.0
+    if kind == "ntk":
+        return ((base * s ** (rot_dim / (rot_dim - 2))) ** (-i / rot_dim)).float(), 1.0
+    n = float(scaling["original_max_position"])
+    if kind == "yarn":
+        def pair(turns):   # the (fractional) pair that turns so many times over n tokens
+            return rot_dim * math.log(n / (turns * 2 * math.pi)) / (2 * math.log(base))
+        lo = max(math.floor(pair(scaling.get("beta_fast", 32.0))), 0)
+        hi = min(math.ceil(pair(scaling.get("beta_slow", 1.0))), rot_dim - 1)
+        ramp = ((i / 2 - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        return (f * (1 - ramp) + f / s * ramp).float(), 0.1 * math.log(s) + 1.0 if s > 1 else 1.0
+    if kind == "bands":
+        low, high = scaling.get("low_freq_factor", 1.0), scaling.get("high_freq_factor", 4.0)
+        keep = ((n * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        return (f * keep + f / s * (1 - keep)).float(), 1.0
+    raise ValueError(f"unknown scaling {kind!r}")
+
+
+class KVCache:
+    """A 4-bit KV cache in pages of `pool` (lora_pool_alloc_pages) and the device tensors of a step.
+
+    One block of `block_tokens` tokens of one layer lives in a page; a model keeps one KVCache per layer (on one pool or
+    several).  A request is a row of the block table: begin() runs lora_kv_layout over the rows' lengths, handing
+    out reserved pages; append() and attend() (or prompt_attend()) are the layer's calls; free() gives the pages of
+    finished rows back to the pool."""
+
+    def __init__(self, pool: B.Pool, q_heads: int, kv_heads: int, head_dim: int, block_tokens: int, max_requests: int,
+                 max_len: int, max_tokens: int, max_q_len: int = 1, dtype=torch.bfloat16):
+        page_bytes = B.PAGE_ROWS * pool.width * 2
+        need = B.lora_kv_block_bytes(kv_heads, head_dim, block_tokens)
+        if need == 0 or need > page_bytes:
+            raise ValueError(f"a block needs {need} bytes, a page of the pool has {page_bytes}")
+        self.pool, self.q_heads, self.kv_heads, self.head_dim = pool, q_heads, kv_heads, head_dim
+        self.block_tokens, self.max_q_len, self.dtype = block_tokens, max_q_len, dtype
+        n = B.lora_pool_num_pages(pool)
+        self.pages = pool.buf.view(-1).view(torch.uint8)[:n * page_bytes].view(n, page_bytes)
+        dev = self.device = pool.buf.device
+        i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=dev)  # noqa: E731
+        self.block_table = i32(max_requests, -(-max_len // block_tokens)).fill_(-1)
+        self.cu_new, self.kv_len = i32(max_requests + 1), i32(max_requests)
+        self.positions, self.slots, self.ids = i32(max_tokens), i32(max_tokens), i32(max_tokens)
+        self.free_list = i32(0)
+        self.head, self._next_head = i32(1), i32(1)
+        self.err = i32(1)
+        self.ws = torch.empty(B.lora_kv_attend_workspace_size(q_heads, kv_heads, head_dim, max_q_len), dtype=torch.uint8,
+                              device=dev)
+
+    def reserve(self, n: int) -> None:
+        """Take n pages of the pool for the steps to come.  Synchronises: the unused part of the list is kept."""
+        ids = B.lora_pool_alloc_pages(self.pool, n)
+        self.free_list = torch.cat([self.free_list[int(self.head.item()):], ids.to(self.device)])
+        self.head.zero_()
+
+    def begin(self, past_len, new_len, req_ids=None, stream=None) -> None:
+        """lora_kv_layout over rows 0 .. R-1 of the block table (past_len, new_len, req_ids [R] int32 on the device)."""
+        R = past_len.numel()
+        B.lora_kv_layout(past_len, new_len, req_ids, self.block_tokens, self.block_table[:R], self.free_list, self.head,
+                         self.cu_new[:R + 1], self.kv_len[:R], self.positions, self.slots, self.ids, self._next_head,
+                         err=self.err, stream=stream)
+        self.head, self._next_head = self._next_head, self.head
+        self.rows = R
+
+    def append(self, q, k, v, inv_freq, q_out, k_out=None, v_out=None, interleaved=False, mscale=1.0, stream=None) -> None:
+        T = k.shape[0]
+        B.lora_kv_append(q, k, v, self.positions[:T], inv_freq, self.slots[:T], self.pages, self.block_tokens, q_out, k_out,
+                         v_out, interleaved=interleaved, mscale=mscale, dtype=self.dtype, err=self.err, stream=stream)
+
+    def attend(self, q, out, scale: Optional[float] = None, lse=None, stream=None) -> None:
+        R = self.rows
+        B.lora_kv_attend(q, self.pages, self.block_tokens, self.kv_heads, self.block_table[:R], self.cu_new[:R + 1],
+                         self.kv_len[:R], self.max_q_len, self.head_dim ** -0.5 if scale is None else scale, out, self.ws,
+                         lse=lse, err=self.err, stream=stream)
+
+    def prompt_attend(self, q, k, v, out, scale: Optional[float] = None, lse=None, stream=None) -> None:
+        """Attention among the step's own rows: requests whose past is empty."""
+        cu = self.cu_new[:self.rows + 1]
+        B.lora_prompt_attend(q, k, v, cu, cu, self.head_dim ** -0.5 if scale is None else scale, out, lse=lse, err=self.err,
+                             stream=stream)
+
+    def free(self, rows) -> None:
+        """Return the pages of finished requests' rows to the pool and clear the rows.  Synchronises."""
+        held = self.block_table[rows].flatten().cpu()
+        B.lora_pool_free_page_list(self.pool, held[held >= 0])
+        self.block_table[rows] = -1

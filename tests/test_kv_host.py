@@ -173,3 +173,28 @@ def test_reference_quantiser_and_page_format():
     assert b[0].max() == 0
     got = c.read(49, 1, 1)
     assert all((a == w).all() for a, w in zip(got, (n[0, 0], s[0, 0], lo[0, 0])))
+
+
+def test_rope_frequencies():
+    """Closed forms of the scalings."""
+    import math
+    from heterogeneous_adapter_batching_b200 import rope_frequencies as rf
+    f, m = rf(128)
+    assert f.shape == (64,) and f[0] == 1 and m == 1.0 and abs(float(f[32]) - 10000.0 ** -0.5) < 1e-9
+    lin, _ = rf(128, scaling={"kind": "linear", "factor": 4.0})
+    assert torch.equal(lin, f / 4)
+    ntk, _ = rf(128, scaling={"kind": "ntk", "factor": 4.0})
+    assert ntk[0] == 1 and abs(float(ntk[-1] / f[-1]) - 0.25) < 1e-6
+    y, m = rf(128, scaling={"kind": "yarn", "factor": 8.0, "original_max_position": 4096})
+    assert abs(m - (0.1 * math.log(8) + 1)) < 1e-12 and y[0] == f[0] and abs(float(y[-1] / f[-1]) - 0.125) < 1e-6
+    assert (y <= f).all() and (y >= f / 8 * (1 - 1e-6)).all()
+    b, _ = rf(128, 500000.0, {"kind": "bands", "factor": 8.0, "original_max_position": 8192})
+    g, _ = rf(128, 500000.0)
+    wave = 2 * math.pi / g.double()
+    assert torch.equal(b[wave < 8192 / 4], g[wave < 8192 / 4])
+    slow = wave > 8192
+    assert ((b[slow] * 8 / g[slow] - 1).abs() < 1e-6).all()
+    with pytest.raises(ValueError):
+        rf(63)
+    with pytest.raises(ValueError):
+        rf(64, scaling={"kind": "other", "factor": 2.0, "original_max_position": 1})
