@@ -212,6 +212,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int toks = kM / a.pk, sh = __ffs(toks), lpk = __ffs(a.pk) - 1;   // tokens of a tile; log2 of a pair's, of the heads'
 
+    Req q{0, 0, 0, 0};   // warp 3: the lane's request
+    if (warp == 3 && a.R <= 32 && lane < a.R) q = request(a, lane);
+    if (warp == 2 && lane < 3) {
+        const CUtensorMap *m = lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+    }
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
             ptx::mbar_init(&sm.full[s], 1);
@@ -240,27 +246,31 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     __syncthreads();
     fence_after();
     const uint32_t tmem = sm.tmem;
-    // The classes of work: items of x key tiles are class x / width.
-    int most = 0;
-    for (int r = tid; r < a.R; r += kThreads) {
-        const Req q = request(a, r);
-        if (q.nq < 0 && blockIdx.x == 0 && a.err) atomicOr(a.err, LORA_DEV_ERR_BAD_LENGTH);
-        if (q.nq > 0) most = max(most, tiles_to(q, q.nq - 1));
-    }
-    if (most > 0) atomicMax(&sm.most, most);
-    __syncthreads();
-    const int width = sm.most / kClasses + 1;
-    for (int r = tid; r < a.R; r += kThreads) {
-        const Req q = request(a, r);
-        if (q.nq <= 0) continue;
-        int from = 0;
-        for (int b = 0; b < kClasses; ++b) {
-            const int to = b + 1 == kClasses ? (q.nq - 1 >> sh) + 1 : first_pair(q, (b + 1) * width, sh);
-            if (to > from) atomicAdd(&sm.hist[b], to - from);
-            from = to;
+    // The classes of work: items of x key tiles are class x / width.  Up to 32 requests are one warp's affair (warp 3); with
+    // more, the CTA counts the tile pairs of each class first.
+    const bool few = a.R <= 32;
+    if (!few) {
+        int most = 0;
+        for (int r = tid; r < a.R; r += kThreads) {
+            const Req q = request(a, r);
+            if (q.nq < 0 && blockIdx.x == 0 && a.err) atomicOr(a.err, LORA_DEV_ERR_BAD_LENGTH);
+            if (q.nq > 0) most = max(most, tiles_to(q, q.nq - 1));
         }
+        if (most > 0) atomicMax(&sm.most, most);
+        __syncthreads();
+        const int width = sm.most / kClasses + 1;
+        for (int r = tid; r < a.R; r += kThreads) {
+            const Req q = request(a, r);
+            if (q.nq <= 0) continue;
+            int from = 0;
+            for (int b = 0; b < kClasses; ++b) {
+                const int to = b + 1 == kClasses ? (q.nq - 1 >> sh) + 1 : first_pair(q, (b + 1) * width, sh);
+                if (to > from) atomicAdd(&sm.hist[b], to - from);
+                from = to;
+            }
+        }
+        __syncthreads();
     }
-    __syncthreads();
 
     // Every role reads the items in order.
     uint32_t items = 0;
@@ -284,32 +294,38 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 3) {
-            int cls = kClasses - 1, r0 = 0;       // where the list is: class, block of 32 requests,
+            int r0 = 0;                           // where the list is: class, block of 32 requests,
             long long before = 0;                 // pairs listed before this block
             int cnt = 0, run = 0, lo = 0;         // this lane's request: pairs in the class, their inclusive sum, the first of them
-            Req q{};
             bool fresh = true;
-            uint32_t n = 0;
-            for (;; ++n) {
+            int cls = kClasses - 1, width;
+            if (few) {
+                if (q.nq < 0 && blockIdx.x == 0 && a.err) atomicOr(a.err, LORA_DEV_ERR_BAD_LENGTH);
+                int most = q.nq > 0 ? tiles_to(q, q.nq - 1) : 0;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) most = max(most, __shfl_xor_sync(~0u, most, d));
+                // the pairs of one request are in order already
+                width = a.R == 1 ? most + 1 : most / kClasses + 1;
+                cls = most / width;               // the classes above are empty
+            } else {
+                width = sm.most / kClasses + 1;
+            }
+            for (uint32_t n = 0;; ++n) {
                 // every other round of items backwards: a CTA's largest item of one round goes with its smallest of the next
-                const long long k = (long long)n * gridDim.x + ((n & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-                const long long want = k / a.groups;
+                const uint32_t k = n * gridDim.x + ((n & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x), want = k / a.groups;
                 Item it{0, -1, 0, 0, 0, 0};
                 while (cls >= 0) {
-                    if (r0 == 0 && fresh && before + sm.hist[cls] <= want) {   // the class as a whole is behind
+                    if (!few && r0 == 0 && fresh && before + sm.hist[cls] <= want) {   // the class as a whole is behind
                         before += sm.hist[cls];
                         --cls;
                         continue;
                     }
                     if (fresh) {
-                        const int r = r0 + lane;
+                        if (!few) q = r0 + lane < a.R ? request(a, r0 + lane) : Req{0, 0, 0, 0};
                         cnt = 0;
-                        if (r < a.R) {
-                            q = request(a, r);
-                            if (q.nq > 0) {
-                                lo = first_pair(q, cls * width, sh);
-                                cnt = (cls + 1 == kClasses ? (q.nq - 1 >> sh) + 1 : first_pair(q, (cls + 1) * width, sh)) - lo;
-                            }
+                        if (q.nq > 0) {
+                            lo = first_pair(q, cls * width, sh);
+                            cnt = (cls + 1 == kClasses ? (q.nq - 1 >> sh) + 1 : first_pair(q, (cls + 1) * width, sh)) - lo;
                         }
                         run = cnt;
 #pragma unroll
@@ -618,6 +634,7 @@ int launch(const PromptArgs &a, cudaStream_t st) {
     k.groups = a.hq / k.pk;
     const int pair = 2 * kM / k.pk;                                     // tokens of a CTA
     const long long items = ((long long)a.Tq / pair + a.R) * k.groups;  // at least the tile pairs of any row ranges
+    if (items > INT32_MAX / 2) return LORA_ERR_TOO_LARGE;
     Maps maps;
     // without keys nothing is loaded: any valid address serves
     const Rows kr = a.Tk > 0 ? a.k : a.q, vr = a.Tk > 0 ? a.v : a.q;
