@@ -33,14 +33,25 @@
 // powers of two): weights then reach at most 2^10 * 32 in fp16, and the usual
 // granule needs no reduction over the warp for its maximum.
 //
-// Work split: a unit is 4 granules (64 tokens) of one (request, kv head, column
-// tile); the units of the batch are numbered and every CTA takes an equal
+// Work split: a unit is 8 granules (128 tokens) of one (request, kv head, column
+// tile), two for each of 4 warps; the units of the batch are numbered and every CTA takes an equal
 // contiguous range, whatever the lengths.  Inside a CTA, 4 warps take granules
 // in turn, each with its own ring of cp.async stages that runs ahead across
 // (request, head) borders, and are joined in shared memory at the end of a
 // piece.  A piece that is not a whole (request, head, tile) leaves its sums in
 // the workspace (at most two per CTA: its first and its last), and a second
-// launch joins those in order.
+// launch joins those in order.  (Joining by whichever CTA counts itself last
+// saved nothing: 25.4 against 23.1 us for one request, 54.5 against 47.9 us for
+// 48 requests of up to 4 tokens, as the main loop spills more registers.)
+//
+// Measured, 32 / 8 heads of 128, bf16: 32 requests of 8192 tokens 78 us, 3.9 TB/s
+// or 59 % of a copy's rate; 128 requests of 1 to 16384 tokens 64 us (47 %); one of
+// 32749 tokens 23 us.  It is bound by issue slots and latency at 12 warps an SM:
+// 342 instructions a granule and warp, of which 64 products; memory would allow
+// 46 us.  Two granules a warp and step at 3 CTAs an SM: one granule at 4 CTAs takes
+// 86 to 90 us, four at 2 CTAs 75 us but 1.5 times as long for short requests.
+// Short requests cost their pieces' beginning and end, about 5 us each and CTA
+// (1024 requests of 64 tokens: 92 us).
 #include <type_traits>
 
 #include "lora_internal.cuh"
@@ -59,8 +70,9 @@ constexpr int kShift = 5;                          // weights are scaled by 2^kS
 constexpr int kJoinThreads = 512;
 
 // What a CTA leaves for the joining kernel about the segment that begins in it and ends in CTA `last`.
-struct Split {
-    int r, h, ct, last;   // last = 0: none
+struct alignas(16) Split {
+    int last, h, gc0, cols;   // last = 0: none; gc0: its first column, cols: its columns
+    int q0, pad[3];           // the request's first query
 };
 
 template <int DIM, int NT, int U>
@@ -242,7 +254,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attend_kernel(At
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int G = a.hq / a.c.heads;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining launch waits for this one's end by itself
     // Units of the batch and this CTA's range of them.
     const int per = (a.R + kThreads - 1) / kThreads, ra = min(a.R, tid * per), rb = min(a.R, ra + per);
     long long mine = 0;
@@ -742,28 +753,31 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attend_kernel(At
             long long last = ((end + 1) * ctas + total - 1) / total - 1;   // the CTA whose range holds `end`
             while (total * (last + 1) / ctas <= end) ++last;
             while (total * last / ctas > end) --last;
-            split[blockIdx.x] = Split{cur.r, cur.h, cur.ct, (int)last};
+            split[blockIdx.x] = Split{(int)last, cur.h, cur.ct * NC, min(NC, cur.q.nq * G - cur.ct * NC), cur.q.q0, {}};
         }
         first_piece = false;
         if (!again) break;
     }
     cp_wait<0>();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // here, not at the start: waiting CTAs take slots (14.5 against 13.8 us)
 }
 
-// Joins the pieces of the segment that begins in CTA blockIdx.x, in order: a warp (two with 8 columns) per column, its
-// lanes DIM / 32 dimensions each.
+// Joins the pieces of the segment that begins in CTA blockIdx.x, in order: the warps are dealt out to the columns that
+// there are (4 query heads of one token: 4 warps each), a lane has DIM / 32 dimensions.  What it costs is a chain of
+// latencies - its launch, Split, the maxima, the sums - about 6 of the 23 us of one request of 32749 tokens.
 template <int DIM, int NT, bool BF>
 __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, const Split *split, const float *part) {
     using H = typename std::conditional<BF, __nv_bfloat16, __half>::type;
-    constexpr int NC = 8 * NT, E = DIM / 32, W = kJoinThreads / 32 / NC;   // W: warps of a column
-    __shared__ float sm_o[W][NC][DIM], sm_l[W][NC];
+    constexpr int NC = 8 * NT, E = DIM / 32, kJoinWarps = kJoinThreads / 32;
+    __shared__ float sm_o[kJoinWarps][DIM], sm_l[kJoinWarps];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Split s = split[blockIdx.x];
     if (s.last == 0) return;
     const int G = a.hq / a.c.heads, first = blockIdx.x, n = s.last - first + 1;
-    const int lane = threadIdx.x & 31, col = (threadIdx.x >> 5) % NC, w = (threadIdx.x >> 5) / NC;
-    const int q0 = a.cu_q[s.r], nq = a.cu_q[s.r + 1] - q0, gc = s.ct * NC + col;
-    if (W == 1 && gc >= nq * G) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int cols = s.cols, W = kJoinWarps / cols;   // W: warps of a column
+    const int col = warp % cols, w = warp / cols;
+    if (W == 1 && w > 0) return;
     // piece i: the second slot of the first CTA, the first slot of the others
     const auto at = [&](int i) { return part + (size_t)(2 * (first + i) + (i == 0)) * partial_floats(DIM, NC); };
     float mm = -INFINITY;
@@ -773,7 +787,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, con
     const float ref = mm == -INFINITY ? 0.f : mm;
     float x[E] = {}, ll = 0.f;
 #pragma unroll 8
-    for (int i = w; i < n; i += W) {
+    for (int i = w < W ? w : n; i < n; i += W) {
         const float *p = at(i);
         const float f = ex2(p[NC * DIM + col] - ref);
         ll = fmaf(f, p[NC * DIM + NC + col], ll);
@@ -791,26 +805,25 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, con
     }
     if (W > 1) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) sm_o[w][col][lane * E + e] = x[e];
-        if (lane == 0) sm_l[w][col] = ll;
+        for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = x[e];
+        if (lane == 0) sm_l[warp] = ll;
         __syncthreads();
-        if (w != 0 || gc >= nq * G) return;
-#pragma unroll
+        if (w != 0) return;
         for (int k = 1; k < W; ++k) {
-            ll += sm_l[k][col];
+            ll += sm_l[k * cols + col];
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] += sm_o[k][col][lane * E + e];
+            for (int e = 0; e < E; ++e) x[e] += sm_o[k * cols + col][lane * E + e];
         }
     }
-    const int qi = gc / G, head = s.h * G + gc - qi * G;
+    const int gc = s.gc0 + col, qi = gc / G, head = s.h * G + gc - qi * G;
     const float inv = ll == 0.f ? 0.f : 1.f / ll;
-    H *out = reinterpret_cast<H *>(a.o.p) + (long long)(q0 + qi) * a.o.ts + (long long)head * a.o.hs + lane * E;
+    H *out = reinterpret_cast<H *>(a.o.p) + (long long)(s.q0 + qi) * a.o.ts + (long long)head * a.o.hs + lane * E;
     alignas(8) H y[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) y[e] = (H)(x[e] * inv);
     if (E == 4) *reinterpret_cast<uint2 *>(out) = *reinterpret_cast<const uint2 *>(y);
     else *reinterpret_cast<uint32_t *>(out) = *reinterpret_cast<const uint32_t *>(y);
-    if (a.lse && lane == 0) a.lse[(size_t)(q0 + qi) * a.hq + head] = ll == 0.f ? -INFINITY : 0.6931471805599453f * (ref + log2f(ll));
+    if (a.lse && lane == 0) a.lse[(size_t)(s.q0 + qi) * a.hq + head] = ll == 0.f ? -INFINITY : 0.6931471805599453f * (ref + log2f(ll));
 }
 
 int tiles_of(int hq, int hkv, int max_q) { return (long long)max_q * (hq / hkv) <= 8 ? 1 : 2; }
