@@ -475,8 +475,11 @@ def lora_kv_layout(past_len, new_len, req_ids, block_tokens: int, block_table, f
     if block_table.dim() != 2 or positions.dim() != 1:
         _refuse(n, "block_table is [R, max_blocks], positions [T]")
     R, T, width = past_len.numel(), positions.numel(), block_table.shape[1]
+    free = _i(n, free_pages, dev, 0)
+    if free == 0:   # an empty list is a list: any address that is not null, nothing is read there
+        free = new_len.data_ptr()
     _run(n, dev, stream, _i(n, past_len, dev, R), _i(n, new_len, dev, R), _i(n, req_ids, dev, R), R, T, block_tokens,
-         _i(n, block_table, dev, R * width), width, _i(n, free_pages, dev, 0), 0 if free_pages is None else free_pages.numel(),
+         _i(n, block_table, dev, R * width), width, free, 0 if free_pages is None else free_pages.numel(),
          _i(n, free_head, dev, 1), _i(n, cu_new, dev, R + 1), _i(n, kv_len, dev, R), _i(n, positions, dev, T),
          _i(n, slots, dev, T), _i(n, ids, dev, T), _i(n, free_head_out, dev, 1), _i(n, err, dev, 1))
 

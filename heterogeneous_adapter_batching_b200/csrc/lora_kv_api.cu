@@ -21,6 +21,21 @@ bool rows_ok(const lora_rows_t *r, int heads, int dtype) {
     return r->token_stride % e == 0 && r->head_stride % e == 0;
 }
 
+// Output rows: also apart from one another.
+bool out_ok(const lora_rows_t *r, int T, int heads, int dim, int dtype) {
+    return rows_ok(r, heads, dtype) && (heads == 0 || ((T < 2 || r->token_stride >= dim) && (heads < 2 || r->head_stride >= dim)));
+}
+
+// n int32 of an array; none where there is no array.
+struct Span {
+    const int32_t *p;
+    long long n;
+};
+bool overlap(const Span &a, const Span &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && x < y + 4 * (uintptr_t)b.n && y < x + 4 * (uintptr_t)a.n;
+}
+
 // Strides that a TMA descriptor takes: positive where they count, below 2^40 bytes (of 16-bit elements).
 bool strides_ok(const lora_rows_t *r, int T, int heads) {
     if (T < 1) return true;
@@ -70,8 +85,17 @@ int lora_kv_layout(const int32_t *past_len, const int32_t *new_len, const int32_
         T < 0 || max_blocks < 1 || num_free < 0)
         return LORA_ERR_INVALID_ARG;
     if (block_tokens < 1 || block_tokens > 1024 || block_tokens % LORA_KV_GRANULE) return LORA_ERR_INVALID_ARG;
-    if (free_head_out && free_head_out == free_head) return LORA_ERR_INVALID_ARG;
     if (R > LORA_KV_MAX_REQUESTS || ((long long)max_blocks + 1) * block_tokens > INT32_MAX) return LORA_ERR_TOO_LARGE;
+    // Every CTA reads the inputs for itself while others write: a kv_len that is past_len would be read half updated.
+    const Span in[] = {{past_len, R}, {new_len, R}, {req_ids, R}, {free_pages, num_free}, {free_head, 1}};
+    const Span out[] = {{block_table, (long long)R * max_blocks}, {cu_new, R + 1}, {kv_len, R}, {positions, T}, {slots, T},
+                        {ids, T}, {free_head_out, 1}};
+    for (const Span &o : out) {
+        for (const Span &i : in)
+            if (overlap(o, i)) return LORA_ERR_INVALID_ARG;
+        for (const Span &i : out)
+            if (&i != &o && overlap(o, i)) return LORA_ERR_INVALID_ARG;
+    }
     const LayoutArgs a{past_len, new_len, req_ids, R, T, block_tokens, block_table, max_blocks, free_pages, num_free,
                        free_head, cu_new, kv_len, positions, slots, ids, free_head_out, err_dev};
     return launch_kv_layout(a, reinterpret_cast<cudaStream_t>(stream));
@@ -84,8 +108,8 @@ int lora_rope(const lora_rows_t *q, int q_heads, const lora_rows_t *k, int k_hea
     if (!rope_ok(src_dtype, dst_dtype, T, head_dim, positions, inv_freq, rot_dim) || q_heads < 0 || k_heads < 0 ||
         q_heads > 4096 || k_heads > 4096)
         return LORA_ERR_INVALID_ARG;
-    if (!rows_ok(q, q_heads, src_dtype) || !rows_ok(k, k_heads, src_dtype) || !rows_ok(q_out, q_heads, dst_dtype) ||
-        !rows_ok(k_out, k_heads, dst_dtype))
+    if (!rows_ok(q, q_heads, src_dtype) || !rows_ok(k, k_heads, src_dtype) || !out_ok(q_out, T, q_heads, head_dim, dst_dtype) ||
+        !out_ok(k_out, T, k_heads, head_dim, dst_dtype))
         return LORA_ERR_INVALID_ARG;
     if (T == 0 || q_heads + k_heads == 0) return LORA_OK;
     RopeArgs a{};
@@ -108,8 +132,8 @@ int lora_kv_append(const lora_rows_t *q, int q_heads, const lora_rows_t *k, cons
         (T > 0 && !slots))
         return LORA_ERR_INVALID_ARG;
     if (!rows_ok(q, q_heads, src_dtype) || !rows_ok(k, h, src_dtype) || !rows_ok(v, h, src_dtype) ||
-        !rows_ok(q_out, q_heads, dst_dtype) || !rows_ok(k_out, k_out ? h : 0, dst_dtype) ||
-        !rows_ok(v_out, v_out ? h : 0, dst_dtype))
+        !out_ok(q_out, T, q_heads, kv->head_dim, dst_dtype) || !out_ok(k_out, T, k_out ? h : 0, kv->head_dim, dst_dtype) ||
+        !out_ok(v_out, T, v_out ? h : 0, kv->head_dim, dst_dtype))
         return LORA_ERR_INVALID_ARG;
     if (T == 0) return LORA_OK;
     RopeArgs a{};
@@ -127,7 +151,8 @@ int lora_kv_gather(const lora_kv_cache_t *kv, const int32_t *slots, int T, const
     reset_launch_count();
     if (int rc = check_cache(kv)) return rc;
     if (dst_dtype < LORA_BF16 || dst_dtype > LORA_FP32 || T < 0 || (T > 0 && !slots)) return LORA_ERR_INVALID_ARG;
-    if (!rows_ok(k_out, k_out ? kv->kv_heads : 0, dst_dtype) || !rows_ok(v_out, v_out ? kv->kv_heads : 0, dst_dtype))
+    if (!out_ok(k_out, T, k_out ? kv->kv_heads : 0, kv->head_dim, dst_dtype) ||
+        !out_ok(v_out, T, v_out ? kv->kv_heads : 0, kv->head_dim, dst_dtype))
         return LORA_ERR_INVALID_ARG;
     if (T == 0 || (!k_out && !v_out)) return LORA_OK;
     const GatherKvArgs a{cache(kv), kv->head_dim, T, slots, rows(k_out), rows(v_out), k_out != nullptr, v_out != nullptr,
@@ -158,7 +183,8 @@ int lora_kv_attend(const lora_rows_t *q, int T, int q_heads, int dtype, const lo
         ws_bytes < attend_workspace(q_heads, kv->kv_heads, kv->head_dim, max_q_len))
         return LORA_ERR_WORKSPACE;
     if (T == 0) return LORA_OK;
-    if (!rows_ok(q, q_heads, dtype) || !rows_ok(out, q_heads, dtype)) return LORA_ERR_INVALID_ARG;
+    if ((long long)T * (q_heads / kv->kv_heads) > INT32_MAX) return LORA_ERR_TOO_LARGE;
+    if (!rows_ok(q, q_heads, dtype) || !out_ok(out, T, q_heads, kv->head_dim, dtype)) return LORA_ERR_INVALID_ARG;
     const AttendArgs a{rows(q), rows(out), T, q_heads, kv->head_dim, dtype, cache(kv), block_table, max_blocks, cu_q,
                        kv_len, R, max_q_len, scale, lse, ws, err_dev};
     return launch_kv_attend(a, reinterpret_cast<cudaStream_t>(stream));
@@ -171,9 +197,9 @@ int lora_prompt_attend(const lora_rows_t *q, const lora_rows_t *k, const lora_ro
     if (!half_type(dtype) || Tq < 0 || Tk < 0 || R < 1 || !group_ok(q_heads, kv_heads) ||
         (head_dim != 64 && head_dim != 128) || !cu_q || !cu_k || !(scale >= 0.f && scale < INFINITY))
         return LORA_ERR_INVALID_ARG;
-    if (R > LORA_KV_MAX_REQUESTS) return LORA_ERR_TOO_LARGE;
+    if (R > LORA_KV_MAX_REQUESTS || (long long)Tq * (q_heads / kv_heads) > INT32_MAX) return LORA_ERR_TOO_LARGE;
     if (Tq == 0) return LORA_OK;
-    if (!rows_ok(q, q_heads, dtype) || !rows_ok(out, q_heads, dtype) || !rows_ok(k, Tk ? kv_heads : 0, dtype) ||
+    if (!rows_ok(q, q_heads, dtype) || !out_ok(out, Tq, q_heads, head_dim, dtype) || !rows_ok(k, Tk ? kv_heads : 0, dtype) ||
         !rows_ok(v, Tk ? kv_heads : 0, dtype))
         return LORA_ERR_INVALID_ARG;
     if (!strides_ok(q, Tq, q_heads) || !strides_ok(k, Tk, kv_heads) || !strides_ok(v, Tk, kv_heads)) return LORA_ERR_INVALID_ARG;

@@ -60,7 +60,11 @@ class KVCache:
     One block of `block_tokens` tokens of one layer lives in a page; a model keeps one KVCache per layer (on one pool or
     several).  A request is a row of the block table: begin() runs lora_kv_layout over the rows' lengths, handing
     out reserved pages; append() and attend() (or prompt_attend()) are the layer's calls; free() gives the pages of
-    finished rows back to the pool."""
+    finished rows back to the pool.
+
+    The calls of a step may be captured in a graph and replayed: every tensor keeps its place, reserve() and free()
+    between replays included.  Steps of one KVCache follow one another on one stream (they share its workspace).
+    Requests that bring more than max_q_len tokens in a step go through prompt_attend()."""
 
     def __init__(self, pool: B.Pool, q_heads: int, kv_heads: int, head_dim: int, block_tokens: int, max_requests: int,
                  max_len: int, max_tokens: int, max_q_len: int = 1, dtype=torch.bfloat16):
@@ -77,25 +81,35 @@ class KVCache:
         self.block_table = i32(max_requests, -(-max_len // block_tokens)).fill_(-1)
         self.cu_new, self.kv_len = i32(max_requests + 1), i32(max_requests)
         self.positions, self.slots, self.ids = i32(max_tokens), i32(max_tokens), i32(max_tokens)
-        self.free_list = i32(0)
-        self.head, self._next_head = i32(1), i32(1)
+        # pages in reserve: free_list[head:], so that its end, which lora_kv_layout is told, never moves
+        self.free_list = i32(n)
+        self.head, self._next_head = i32(1).fill_(n), i32(1).fill_(n)
+        self.rows = 0
         self.err = i32(1)
         self.ws = torch.empty(B.lora_kv_attend_workspace_size(q_heads, kv_heads, head_dim, max_q_len), dtype=torch.uint8,
                               device=dev)
 
     def reserve(self, n: int) -> None:
-        """Take n pages of the pool for the steps to come.  Synchronises: the unused part of the list is kept."""
+        """Take n pages of the pool for the steps to come.  Synchronises the device."""
+        torch.cuda.synchronize(self.device)
         ids = B.lora_pool_alloc_pages(self.pool, n)
-        self.free_list = torch.cat([self.free_list[int(self.head.item()):], ids.to(self.device)])
-        self.head.zero_()
+        kept = self.free_list[int(self.head.item()):]
+        both = torch.cat([kept, ids.to(self.device)])
+        self.free_list[self.free_list.numel() - both.numel():] = both
+        self.head.fill_(self.free_list.numel() - both.numel())
+        torch.cuda.synchronize(self.device)
 
     def begin(self, past_len, new_len, req_ids=None, stream=None) -> None:
-        """lora_kv_layout over rows 0 .. R-1 of the block table (past_len, new_len, req_ids [R] int32 on the device)."""
+        """lora_kv_layout over rows 0 .. R-1 of the block table (past_len, new_len, req_ids [R] int32 on the device;
+        past_len is not this object's kv_len, which the call writes)."""
         R = past_len.numel()
         B.lora_kv_layout(past_len, new_len, req_ids, self.block_tokens, self.block_table[:R], self.free_list, self.head,
                          self.cu_new[:R + 1], self.kv_len[:R], self.positions, self.slots, self.ids, self._next_head,
                          err=self.err, stream=stream)
-        self.head, self._next_head = self._next_head, self.head
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.device)
+        with torch.cuda.stream(stream):       # None: the current one
+            self.head.copy_(self._next_head)
         self.rows = R
 
     def append(self, q, k, v, inv_freq, q_out, k_out=None, v_out=None, interleaved=False, mscale=1.0, stream=None) -> None:
@@ -116,7 +130,11 @@ class KVCache:
                              stream=stream)
 
     def free(self, rows) -> None:
-        """Return the pages of finished requests' rows to the pool and clear the rows.  Synchronises."""
-        held = self.block_table[rows].flatten().cpu()
+        """Return the pages of finished requests' rows to the pool and clear the rows.  Synchronises the device."""
+        torch.cuda.synchronize(self.device)
+        done = torch.zeros(self.block_table.shape[0], dtype=torch.bool)
+        done[rows] = True                     # a row that is named twice is freed once
+        held = self.block_table[done.to(self.device)].flatten().cpu()
         B.lora_pool_free_page_list(self.pool, held[held >= 0])
-        self.block_table[rows] = -1
+        self.block_table[done.to(self.device)] = -1
+        torch.cuda.synchronize(self.device)

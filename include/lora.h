@@ -414,8 +414,9 @@ int lora_slot_cache_stats(lora_slot_cache_t c, int64_t *hits, int64_t *misses, i
  * + h * head_stride + d].  data is 16-byte aligned and both strides are
  * multiples of 16 bytes, else LORA_ERR_INVALID_ARG: a column block of a fused
  * projection output is fine.  Strides count elements and are not negative.
- * The rows of an output are distinct and overlap no input, except where a
- * call allows working in place. */
+ * The rows of an output are distinct (its strides at least head_dim where there
+ * is more than one token or head, else LORA_ERR_INVALID_ARG) and overlap no
+ * input, except where a call allows working in place. */
 typedef struct {
     void *data;
     int64_t token_stride;
@@ -468,8 +469,8 @@ size_t lora_kv_block_bytes(int kv_heads, int head_dim, int block_tokens);
  *                    request's req_ids[r], what lora_plan takes (req_ids NULL: -1)
  *   free_head_out [1] (NULL: not wanted) first unused place of free_pages
  * Rows past cu_new[R] get -1 in positions, slots and ids, which every call
- * below and lora_plan skip.  Inputs and outputs must not overlap (free_head_out
- * may not be free_head).  R in 1..LORA_KV_MAX_REQUESTS, T >= 0.
+ * below and lora_plan skip.  Outputs overlap neither inputs nor one another
+ * (LORA_ERR_INVALID_ARG): kv_len is not past_len, free_head_out not free_head.  R in 1..LORA_KV_MAX_REQUESTS, T >= 0.
  * A request fails, alone, when a length is negative or past + new exceeds
  * max_blocks * block_tokens (or its rows exceed T): LORA_DEV_ERR_BAD_LENGTH; or
  * when the list is too short for it: LORA_DEV_ERR_NO_PAGES.  It takes no
@@ -547,7 +548,9 @@ int lora_kv_gather(const lora_kv_cache_t *cache, const int32_t *slots, int T, co
  * Softmax statistics and sums are fp32.  ws: lora_kv_attend_workspace_size
  * bytes, 256-byte aligned, any contents; calls that may overlap on the GPU need
  * workspaces of their own.  q_heads is a multiple of cache->kv_heads, at most
- * LORA_KV_MAX_GROUP times it; R in 1..LORA_KV_MAX_REQUESTS. */
+ * LORA_KV_MAX_GROUP times it; R in 1..LORA_KV_MAX_REQUESTS; T * q_heads /
+ * kv_heads at most INT32_MAX (lora_prompt_attend too), else
+ * LORA_ERR_TOO_LARGE. */
 #define LORA_KV_MAX_GROUP 64
 size_t lora_kv_attend_workspace_size(int q_heads, int kv_heads, int head_dim, int max_q_len);
 int lora_kv_attend(const lora_rows_t *q, int T, int q_heads, int dtype, const lora_kv_cache_t *cache,

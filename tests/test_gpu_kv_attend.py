@@ -131,6 +131,14 @@ def test_several_new_tokens(H, q_lens, lens, hq, hk, dtype, dim):
     check(H, queries(2, sum(q_lens), hq, dim, dtype), pages, table, q_lens, lens, hq, hk, dim, 16, dtype)
 
 
+@pytest.mark.parametrize("R", [129, 300])
+def test_more_requests_than_threads(H, R):
+    lens = np.random.default_rng(R).integers(0, 40, R)
+    new = np.random.default_rng(R + 1).integers(0, 3, R)
+    pages, table = make_cache(R, lens, 1, 64, 16)
+    check(H, queries(R, int(new.sum()), 2, 64, BF), pages, table, list(new), list(lens), 2, 1, 64, 16, BF)
+
+
 def test_max_q_len_above_the_batch(H):
     pages, table = make_cache(1, [50, 9], 2, 128, 16)
     q = queries(3, 3, 8, 128, BF)

@@ -138,7 +138,7 @@ def test_prompts_then_decoding_then_drafts(H):
     after = [model.q.page_rows(int(p)) for p in model.q.page_table.cpu().flatten() if p >= 0]
     assert all(torch.equal(a, b) for a, b in zip(before, after))
     used = int((cache.block_table >= 0).sum())
-    assert used == int((-(-past // BLOCK)).sum()) and int(cache.head.item()) == used
+    assert used == int((-(-past // BLOCK)).sum()) and cache.free_list[int(cache.head.item()):].numel() == 20 - used
     cache.free(list(range(R)))
     assert H.lora_pool_usage(model.q.pool_a) == (adapter_pages, 20 - used) and (cache.block_table == -1).all()
 
@@ -218,4 +218,53 @@ def test_a_decode_step_as_one_graph(H):
             ref.add(r, y[r:r + 1, HQ:HQ + HK], y[r:r + 1, HQ + HK:], torch.tensor([t]), freq)
             if t in (0, 1, 47, 48, 59):
                 check_rows(out, qo, ref, r, r, 1)
-    assert int(cache.err.item()) == 0 and int(heads[0].item()) == 2 * R
+    assert int(cache.err.item()) == 0 and cache.free_list[int(heads[0].item()):].numel() == 10 - 2 * R
+
+
+def test_a_captured_step_of_the_cache_object(H):
+    """begin() replayed hands out new pages every time, and goes on after reserve() and free() between replays."""
+    R = 2
+    buf = torch.empty((40 * 16, 256), dtype=BF, device="cuda")
+    pool = H.lora_pool_create(buf, 256)
+    cache = H.KVCache(pool, HQ, HK, DIM, 16, max_requests=R, max_len=96, max_tokens=R)
+    cache.reserve(2)
+    past, new = i32([0] * R), i32([1] * R)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    cache.begin(past, i32([0] * R), stream=side)          # a first call outside the graph, on another stream
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.begin(past, new)
+        past.add_(new)
+    for t in range(96):
+        if t == 16:
+            cache.reserve(10)
+        g.replay()
+        if t == 15:
+            assert cache.free_list[int(cache.head.item()):].numel() == 0
+    torch.cuda.synchronize()
+    assert int(cache.err.item()) == 0 and cache.slots.tolist() == [16 * int(cache.block_table[r, 5]) + 15 for r in range(R)]
+    pages = cache.block_table.flatten().tolist()
+    assert min(pages) >= 0 and len(set(pages)) == 12
+    cache.free([1, 1])                                    # a row named twice is freed once
+    assert H.lora_pool_usage(pool)[1] == 6 and (cache.block_table[1] == -1).all() and cache.block_table[0].tolist() == pages[:6]
+    past[0], new[0], past[1] = 96, 0, 0
+    cache.reserve(1)
+    g.replay()
+    torch.cuda.synchronize()
+    assert int(cache.err.item()) == 0 and int(cache.block_table[1, 0]) in pages[6:] + [p for p in range(40) if p not in pages]
+
+
+def test_a_cache_without_pages_in_reserve(H):
+    """An empty list of free pages is a list that has run dry, not a complete table."""
+    buf = torch.empty((8 * 16, 256), dtype=BF, device="cuda")
+    cache = H.KVCache(H.lora_pool_create(buf, 256), HQ, HK, DIM, 16, max_requests=1, max_len=32, max_tokens=4)
+    cache.begin(i32([0]), i32([3]))
+    torch.cuda.synchronize()
+    assert int(cache.err.item()) == H.DEV_ERR_NO_PAGES and int(cache.kv_len[0]) == 0 and (cache.slots == -1).all()
+    cu, kl, pos, slots, err = i32([0, 0]), i32([9]), i32([9] * 4), i32([9] * 4), i32([0])
+    table = i32([[5, 5]])
+    H.lora_kv_layout(i32([0]), i32([3]), None, 16, table, i32([]), None, cu, kl, pos, slots, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == H.DEV_ERR_NO_PAGES and table.tolist() == [[5, 5]] and kl.tolist() == [0] and slots.tolist() == [-1] * 4

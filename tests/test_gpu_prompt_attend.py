@@ -102,6 +102,13 @@ def test_prefix_and_fewer_keys_than_rows(H, q_lens, k_lens, hq, hk, dim):
     check(H, q_lens, k_lens, hq, hk, dim, BF, seed=sum(q_lens), step=5)
 
 
+@pytest.mark.parametrize("R", [33, 257, 700])
+def test_many_requests(H, R):
+    n = np.random.default_rng(R).integers(0, 9, R)
+    n[[3, R // 2, R - 1]] = 150, 0, 130
+    check(H, list(n), list(n), 4, 2, 64, BF, seed=R, step=3)
+
+
 def test_rows_outside_the_batch(H):
     check(H, [20, 33], [20, 33], 4, 2, 64, FP, q0=3, k0=11, tail=9)
 

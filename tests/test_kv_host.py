@@ -142,6 +142,47 @@ def test_prompt_refusals(H):
     assert lib.lora_last_launch_count() == 0
 
 
+def test_layout_refuses_arrays_that_overlap(H):
+    lib = H.load_library()
+    R, T, width, nfree = 4, 8, 4, 10
+    names = ("past", "new", "ids_in", "free", "head", "table", "cu", "kv", "pos", "slots", "ids", "out")
+    size = dict(past=R, new=R, ids_in=R, free=nfree, head=1, table=R * width, cu=R + 1, kv=R, pos=T, slots=T, ids=T, out=1)
+
+    def call(**at):
+        a = {k: p(at.get(k, 4096 * (i + 1))) for i, k in enumerate(names)}
+        return lib.lora_kv_layout(a["past"], a["new"], a["ids_in"], R, T, 16, a["table"], width, a["free"], nfree, a["head"], a["cu"],
+                                  a["kv"], a["pos"], a["slots"], a["ids"], a["out"], None, None)
+
+    where = {k: 4096 * (i + 1) for i, k in enumerate(names)}
+    for o in names[5:]:
+        for i in names:
+            if i != o:   # the first and the last word of i
+                assert call(**{o: where[i]}) == -1, (o, i)
+                assert call(**{o: where[i] + 4 * (size[i] - 1)}) == -1, (o, i)
+                assert call(**{o: where[i] - 4 * (size[o] - 1)}) == -1, (o, i)
+    assert lib.lora_last_launch_count() == 0
+
+
+def test_outputs_whose_rows_overlap_are_refused(H):
+    lib = H.load_library()
+    n = H.lora_kv_attend_workspace_size(32, 8, 128, 1)
+    for bad in (dict(ts=0), dict(hs=0), dict(hs=64), dict(ts=64)):
+        o = rows(H, **bad)
+        assert lib.lora_rope(rows(H), 8, None, 0, 0, 4, 128, p(), p(), 128, 0, 1.0, o, None, 0, None) == -1, bad
+        assert lib.lora_rope(rows(H), 8, rows(H), 2, 0, 4, 128, p(), p(), 128, 0, 1.0, rows(H), o, 0, None) == -1, bad
+        for k in range(3):
+            out = [o if i == k else rows(H) for i in range(3)]
+            assert lib.lora_kv_append(rows(H), 8, rows(H), rows(H), 0, 4, p(), p(), 128, 0, 1.0, p(), cache(H), *out, 0, None, None) == -1, bad
+        assert lib.lora_kv_gather(cache(H), p(), 4, o, None, 0, None, None) == -1, bad
+        assert lib.lora_kv_gather(cache(H), p(), 4, None, o, 0, None, None) == -1, bad
+        assert lib.lora_kv_attend(rows(H), 4, 32, 0, cache(H), p(), 4, p(), p(), 4, 1, 1.0, o, None, p(), n, None, None) == -1, bad
+        assert lib.lora_prompt_attend(rows(H), rows(H), rows(H), 4, 4, 32, 8, 128, 0, p(), p(), 1, 1.0, o, None, None, None) == -1, bad
+    # rows times heads of a group beyond 31 bits
+    assert lib.lora_kv_attend(rows(H), 2 ** 30, 32, 0, cache(H), p(), 4, p(), p(), 4, 1, 1.0, rows(H), None, p(), n, None, None) == -8
+    assert lib.lora_prompt_attend(rows(H), rows(H), rows(H), 2 ** 30, 4, 32, 8, 128, 0, p(), p(), 1, 1.0, rows(H), None, None, None) == -8
+    assert lib.lora_last_launch_count() == 0
+
+
 def test_binding_refuses_what_it_cannot_pass(H):
     t = torch.zeros
     q, i = t((4, 8, 128), dtype=torch.bfloat16), t(4, dtype=torch.int32)
