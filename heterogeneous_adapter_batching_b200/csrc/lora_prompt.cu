@@ -36,6 +36,17 @@
 // behind a request's last key in its last tile, warp 3 lists the items, warps 4-7
 // and 8-11 own tile 0 and 1.  Waits are bounded (LORA_DEV_ERR_TIMEOUT).  No
 // cluster multicast.
+//
+// Measured, bf16, 32 / 8 heads of 128: one prompt of 8192 tokens 485 us, 1.13
+// PFLOP/s (a large library product: 1.64); 16 prompts of 16 to 8192 tokens 220 us;
+// 24 of up to 128 tokens 13 us; one of 16 tokens 8 us.  What bounds long prompts
+// is the tensor pipe's start: a product whose 16 instructions should take 1024
+// cycles takes about 1450 when it is issued by itself, as the two products of a
+// tile are (one waits for the exponentials, which keep pace).  Products issued by
+// two warps, weights handed over in halves, a quarter of the exponentials as
+// polynomials, or two threads a row all came out equal or slower (484 to 1020 us
+// at 8192).  Ragged batches lose to diagonal tiles and to rows of short prompts
+// that a tile of 128 does not fill.
 #include <cuda.h>
 
 #include <type_traits>
@@ -83,6 +94,7 @@ struct KArgs {
     float *lse;
     const int32_t *cu_q, *cu_k;
     int Tq, Tk, R, hq, G, pk, groups;   // pk: heads in a tile; groups: tiles' head blocks, hq / pk
+    uint32_t items;   // most items of row ranges that do not overlap
     float scale;
     int32_t *err;
 };
@@ -246,8 +258,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     __syncthreads();
     fence_after();
     const uint32_t tmem = sm.tmem;
-    // The classes of work: items of x key tiles are class x / width.  Up to 32 requests are one warp's affair (warp 3); with
-    // more, the CTA counts the tile pairs of each class first.
+    // The classes of work: items of x key tiles are class x / width.  Up to 32 requests are one warp's affair (warp 3: 24 short
+    // prompts take 13.3 us, 15.7 with the count); with more, where a warp would walk the list once per class, the CTA counts
+    // the tile pairs of each class first.
     const bool few = a.R <= 32;
     if (!few) {
         int most = 0;
@@ -314,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 // every other round of items backwards: a CTA's largest item of one round goes with its smallest of the next
                 const uint32_t k = n * gridDim.x + ((n & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x), want = k / a.groups;
                 Item it{0, -1, 0, 0, 0, 0};
-                while (cls >= 0) {
+                while (cls >= 0 && k < a.items) {
                     if (!few && r0 == 0 && fresh && before + sm.hist[cls] <= want) {   // the class as a whole is behind
                         before += sm.hist[cls];
                         --cls;
@@ -635,6 +648,7 @@ int launch(const PromptArgs &a, cudaStream_t st) {
     const int pair = 2 * kM / k.pk;                                     // tokens of a CTA
     const long long items = ((long long)a.Tq / pair + a.R) * k.groups;  // at least the tile pairs of any row ranges
     if (items > INT32_MAX / 2) return LORA_ERR_TOO_LARGE;
+    k.items = (uint32_t)items;
     Maps maps;
     // without keys nothing is loaded: any valid address serves
     const Rows kr = a.Tk > 0 ? a.k : a.q, vr = a.Tk > 0 ? a.v : a.q;

@@ -212,6 +212,17 @@ def test_bad_row_ranges(H, cu_q, cu_k, skip):
                 assert (np.abs(got[t, g] - o) <= K.out_bound(o, absv, K.row_bound(qv, kk, 0.2), BF, K.HALF[BF])).all()
 
 
+@pytest.mark.parametrize("R", [9, 400])
+def test_row_ranges_that_turn_back_again_and_again(H, R):
+    """Every other request is refused; the others name the same rows over and over.  The call ends, says so, and writes those
+    rows only."""
+    T = 300
+    q, k, v = (rows(90 + i, T + 5, n, 64, BF) for i, n in enumerate((2, 1, 1)))
+    cu = np.arange(R + 1) % 2 * T
+    out, ls, err = run(H, q, k, v, cu, cu, 0.125)
+    assert err == H.DEV_ERR_BAD_LENGTH and (out[T:] == 7).all() and (ls[T:] == 7).all()
+
+
 def test_no_keys_at_all(H):
     q, k = rows(1, 5, 2, 64, BF), torch.empty((0, 1, 64), dtype=BF)
     out, ls, err = run(H, q, k, k, [0, 5], [0, 0], 0.2)
