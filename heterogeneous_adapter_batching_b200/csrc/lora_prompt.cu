@@ -45,7 +45,9 @@
 // tile are (one waits for the exponentials, which keep pace).  Products issued by
 // two warps, weights handed over in halves, a quarter of the exponentials as
 // polynomials, or two threads a row all came out equal or slower (484 to 1020 us
-// at 8192).  Ragged batches lose to diagonal tiles and to rows of short prompts
+// at 8192), and so did scores that do not wait for the product before them (P_t
+// in columns of its own, which leaves room for tiles of 80 keys: 774 us, as twice
+// the starts cost more than the waits).  Ragged batches lose to diagonal tiles and to rows of short prompts
 // that a tile of 128 does not fill.
 #include <cuda.h>
 
@@ -121,21 +123,21 @@ __device__ __forceinline__ void drain_wait(uint64_t *b, uint32_t parity) {
     }
 }
 
-__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 | (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
+// Shared memory descriptors (SW128, 8 rows of 128 bytes apart by 1024): the upper half is a constant, so that the steps through
+// a tile are 32-bit additions.
+constexpr uint32_t kDescHi = 1024u >> 4 | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t sdesc(uint32_t addr, uint32_t lbo) { return ((addr >> 4) & 0x3FFFu) | (lbo >> 4) << 16; }
 // kind::f16 with fp32 accumulators; type 0 = fp16, 1 = bf16.
 constexpr uint32_t idesc(int type, int N, int b_mn) {
     return 1u << 4 | (uint32_t)type << 7 | (uint32_t)type << 10 | (uint32_t)b_mn << 16 | (uint32_t)(N >> 3) << 17 | (uint32_t)(kM >> 4) << 24;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(kDescHi), "r"(id), "r"(acc) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(kDescHi), "r"(id), "r"(acc) : "memory");
 }
 __device__ __forceinline__ void commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
@@ -416,28 +418,35 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         } else if (warp == 1) {
             constexpr uint32_t id_s = idesc(BF ? 1 : 0, kN, 0), id_o = idesc(BF ? 1 : 0, DIM, 1);
             const auto scores = [&](int t, int s) {   // one lane
-                const uint64_t dq = sdesc(ptx::smem_u32(sm.q[t]), 16, 1024), dk = sdesc(ptx::smem_u32(sm.kv[s]), 16, 1024);
+                const uint32_t dq = sdesc(ptx::smem_u32(sm.q[t]), 16), dk = sdesc(ptx::smem_u32(sm.kv[s]), 16);
 #pragma unroll
                 for (int k = 0; k < DIM / 16; ++k) {
-                    const uint64_t off = (k / 4) * (HALF >> 4) + (k % 4) * 2;
+                    const uint32_t off = (k / 4) * (HALF >> 4) + (k % 4) * 2;
                     mma_ss(tmem + t * kN, dq + off, dk + off, id_s, k != 0);
                 }
                 commit(&sm.s_full[t]);
             };
-            const auto await = [&](uint64_t *b, uint32_t parity) { return (bool)__all_sync(~0u, wait(b, parity, sm, a.err)); };
+            // The tensor pipe takes few instructions ahead, so what runs between two products is time that it stands still: no vote
+            // on the outcome of a wait (3 to 7 % of a prompt of 1024 or more).  Lanes that differ about it (a wait that ran out) take the same
+            // steps up to the next item all the same.
+            const auto await = [&](uint64_t *b, uint32_t parity) {
+                const bool r = wait(b, parity, sm, a.err);
+                __syncwarp();
+                return r;
+            };
             Item it;
             int i = 0;                        // ring position of the item's first keys
             uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};
             bool ok = true;
-            while (ok && next_item(it)) {
+            while (__all_sync(~0u, ok) && next_item(it)) {
                 const int nt[2] = {key_tiles(it, 0), key_tiles(it, 1)}, total = max(nt[0], nt[1]);
                 if (total == 0) continue;
                 const int tail_rows = it.nk - (total - 1) * kN;   // rows of the last key tile that are the request's (maybe more than kN)
-                ok = await(&sm.full[i % ST], (i / ST) & 1);
+                ok &= await(&sm.full[i % ST], (i / ST) & 1);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    if (!ok || nt[t] == 0) continue;
-                    ok = await(&sm.q_full[t], qn[t] & 1);
+                    if (nt[t] == 0) continue;
+                    ok &= await(&sm.q_full[t], qn[t] & 1);
                     ++qn[t];
                     if (ok && lane == 0) {
                         fence_after();
@@ -446,29 +455,29 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     }
                 }
                 if (ok && lane == 0) commit(&sm.empty[i % ST]);
-                for (int j = 0; ok && j < total; ++j) {
+                for (int j = 0; j < total; ++j) {
                     const int vi = i + 2 * j + 1, ki = vi + 1, vs = vi % ST, ks = ki % ST;
-                    ok = await(&sm.full[vs], (vi / ST) & 1);
-                    if (ok && j == total - 1 && tail_rows < kN) {
+                    ok &= await(&sm.full[vs], (vi / ST) & 1);
+                    if (j == total - 1 && tail_rows < kN) {
                         // values behind the request's last key: other rows, whatever they hold; 0 x NaN would reach this request
-                        for (int x = tail_rows * 8 + lane; x < kN * 8; x += 32)
+                        for (int x = tail_rows * 8 + lane; ok && x < kN * 8; x += 32)
                             for (int h = 0; h < HALVES; ++h)
                                 *reinterpret_cast<uint4 *>(sm.kv[vs] + h * HALF + x * 16) = make_uint4(0, 0, 0, 0);
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
                     }
-                    if (ok && j + 1 < total) ok = await(&sm.full[ks], (ki / ST) & 1);
-                    const uint64_t dv = sdesc(ptx::smem_u32(sm.kv[vs]), HALF, 1024);
+                    if (j + 1 < total) ok &= await(&sm.full[ks], (ki / ST) & 1);
+                    const uint32_t dv = sdesc(ptx::smem_u32(sm.kv[vs]), HALF);
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        if (!ok || j >= nt[t]) continue;
-                        ok = await(&sm.p_ready[t], pn[t] & 1);
+                        if (j >= nt[t]) continue;
+                        ok &= await(&sm.p_ready[t], pn[t] & 1);
                         ++pn[t];
                         if (ok && lane == 0) {
                             fence_after();
 #pragma unroll
                             for (int k = 0; k < kN / 16; ++k)
-                                mma_ts(tmem + 2 * kN + t * 128, tmem + t * kN + k * 8, dv + (uint64_t)(k * (2048 >> 4)), id_o, j != 0 || k != 0);
+                                mma_ts(tmem + 2 * kN + t * 128, tmem + t * kN + k * 8, dv + k * (2048 >> 4), id_o, j != 0 || k != 0);
                             if (j + 1 < nt[t]) {
                                 scores(t, ks);
                                 if (j + 2 == nt[t]) commit(&sm.q_empty[t]);
