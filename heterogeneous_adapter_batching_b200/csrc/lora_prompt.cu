@@ -37,9 +37,10 @@
 // and 8-11 own tile 0 and 1.  Waits are bounded (LORA_DEV_ERR_TIMEOUT).  No
 // cluster multicast.
 //
-// Measured, bf16, 32 / 8 heads of 128: one prompt of 8192 tokens 485 us, 1.13
-// PFLOP/s (a large library product: 1.64); 16 prompts of 16 to 8192 tokens 220 us;
-// 24 of up to 128 tokens 13 us; one of 16 tokens 8 us.  What bounds long prompts
+// Measured, bf16, 32 / 8 heads of 128: one prompt of 8192 tokens 457 to 513 us with
+// the card's power, 1.07 to 1.20 PFLOP/s (a large library product: 1.64); 16 of
+// 128 to 2048 tokens 180 to 200 us; 64 of 128 tokens 51 us; 24 of up to 97 tokens
+// 12 us; one of 16 tokens 8 us.  What bounds long prompts
 // is the tensor pipe's start: a product whose 16 instructions should take 1024
 // cycles takes about 1450 when it is issued by itself, as the two products of a
 // tile are (one waits for the exponentials, which keep pace).  Products issued by
