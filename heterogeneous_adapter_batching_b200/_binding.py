@@ -397,17 +397,21 @@ def _device(name: str, t: torch.Tensor) -> int:
     return dev
 
 
-def _r(name: str, t: Optional[torch.Tensor], dev: int, dtype, dim: int):
-    """lora_rows_t of a [T, heads, head_dim] tensor (None: a null pointer)."""
-    if t is None:
-        return None
-    n, s = t.shape, t.stride()
-    if len(n) != 3 or n[2] != dim or t.dtype != dtype or t.get_device() != dev:
-        _refuse(name, f"rows [T, heads, {dim}] of {dtype} on cuda:{dev} expected, not {tuple(n)} of {t.dtype} on {t.device}")
-    if s[2] != 1:
+def _dims(name: str, shape):
+    if len(shape) != 3:
+        _refuse(name, f"rows are [T, heads, head_dim], not {tuple(shape)}")
+    return shape
+
+
+def _r(name: str, t: torch.Tensor, dev: int, dtype, shape) -> bytes:
+    """lora_rows_t of a [T, heads, head_dim] tensor of this shape and type."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        _refuse(name, f"rows {tuple(shape)} of {dtype} on cuda:{dev} expected, not {tuple(t.shape)} of {t.dtype} on {t.device}")
+    ts, hs, one = t.stride()
+    if one != 1:
         _refuse(name, "the elements of a row are adjacent")
     # the stride of a dimension of one element says nothing
-    return _ROWS.pack(t.data_ptr(), s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0)
+    return _ROWS.pack(t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0)
 
 
 def _i(name: str, t: Optional[torch.Tensor], dev: int, n: int):
@@ -417,11 +421,6 @@ def _i(name: str, t: Optional[torch.Tensor], dev: int, n: int):
     if t.dtype != torch.int32 or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
         _refuse(name, f"index arrays are contiguous int32 tensors on cuda:{dev} with at least {n} elements")
     return t.data_ptr()
-
-
-def _same(name: str, what: str, a, b):
-    if a != b:
-        _refuse(name, f"{what}: {a} against {b}")
 
 
 def _kv(name: str, pages: torch.Tensor, dev: int, kv_heads: int, head_dim: int, block_tokens: int):
@@ -489,17 +488,20 @@ def lora_rope(q, k, positions, inv_freq, q_out, k_out=None, interleaved: bool = 
     """q [T, q_heads, head_dim] (k likewise, or None with k_out None); inv_freq [rot_dim / 2] fp32 on the device."""
     n = "lora_rope"
     dev, src, dst = _device(n, q), q.dtype, q_out.dtype
-    T, hq, dim = q.shape
-    _same(n, "q_out", q_out.shape, q.shape)
-    if (k is None) != (k_out is None):
-        _refuse(n, "k and k_out come together")
-    if k is not None:
-        _same(n, "k_out", k_out.shape, k.shape)
-        _same(n, "rows of q and k", k.shape[0], T)
+    shape = q.shape
+    T, hq, dim = _dims(n, shape)
+    hk, kr, ko = 0, None, None
+    if k is not None or k_out is not None:
+        if k is None or k_out is None:
+            _refuse(n, "k and k_out come together")
+        kshape = k.shape
+        Tk, hk, dk = _dims(n, kshape)
+        if Tk != T or dk != dim:
+            _refuse(n, f"rows of q and k: {tuple(shape)} against {tuple(kshape)}")
+        kr, ko = _r(n, k, dev, src, kshape), _r(n, k_out, dev, dst, kshape)
     f, rot = _freq(n, inv_freq, dev)
-    _run(n, dev, stream, _r(n, q, dev, src, dim), hq, _r(n, k, dev, src, dim), 0 if k is None else k.shape[1],
-         DTYPES.get(src, -1), T, dim, _i(n, positions, dev, T), f, rot, int(interleaved), mscale,
-         _r(n, q_out, dev, dst, dim), _r(n, k_out, dev, dst, dim), DTYPES.get(dst, -1))
+    _run(n, dev, stream, _r(n, q, dev, src, shape), hq, kr, hk, DTYPES.get(src, -1), T, dim, _i(n, positions, dev, T), f, rot,
+         int(interleaved), mscale, _r(n, q_out, dev, dst, shape), ko, DTYPES.get(dst, -1))
 
 
 def lora_kv_append(q, k, v, positions, inv_freq, slots, pages, block_tokens: int, q_out, k_out=None, v_out=None,
@@ -508,34 +510,39 @@ def lora_kv_append(q, k, v, positions, inv_freq, slots, pages, block_tokens: int
     written, by default that of the outputs (of k when there is none)."""
     n = "lora_kv_append"
     dev, src = _device(n, k), k.dtype
-    T, hk, dim = k.shape
-    dst = dtype or next((x.dtype for x in (q_out, k_out, v_out) if x is not None), src)
-    _same(n, "v", v.shape, k.shape)
-    if (q is None) != (q_out is None):
-        _refuse(n, "q and q_out come together")
-    if q is not None:
-        _same(n, "q_out", q_out.shape, q.shape)
-        _same(n, "rows of q and k", q.shape[0], T)
-    for x in (k_out, v_out):
-        if x is not None:
-            _same(n, "k_out and v_out", x.shape, k.shape)
+    shape = k.shape
+    T, hk, dim = _dims(n, shape)
+    if dtype is None:
+        first = q_out if q_out is not None else k_out if k_out is not None else v_out if v_out is not None else k
+        dtype = first.dtype
+    hq, qr, qo = 0, None, None
+    if q is not None or q_out is not None:
+        if q is None or q_out is None:
+            _refuse(n, "q and q_out come together")
+        qshape = q.shape
+        Tq, hq, dq = _dims(n, qshape)
+        if Tq != T or dq != dim:
+            _refuse(n, f"rows of q and k: {tuple(qshape)} against {tuple(shape)}")
+        qr, qo = _r(n, q, dev, src, qshape), _r(n, q_out, dev, dtype, qshape)
     f, rot = _freq(n, inv_freq, dev)
-    _run(n, dev, stream, _r(n, q, dev, src, dim), 0 if q is None else q.shape[1], _r(n, k, dev, src, dim),
-         _r(n, v, dev, src, dim), DTYPES.get(src, -1), T, _i(n, positions, dev, T), f, rot, int(interleaved), mscale,
-         _i(n, slots, dev, T), _kv(n, pages, dev, hk, dim, block_tokens), _r(n, q_out, dev, dst, dim),
-         _r(n, k_out, dev, dst, dim), _r(n, v_out, dev, dst, dim), DTYPES.get(dst, -1), _i(n, err, dev, 1))
+    _run(n, dev, stream, qr, hq, _r(n, k, dev, src, shape), _r(n, v, dev, src, shape), DTYPES.get(src, -1), T,
+         _i(n, positions, dev, T), f, rot, int(interleaved), mscale, _i(n, slots, dev, T),
+         _kv(n, pages, dev, hk, dim, block_tokens), qo, None if k_out is None else _r(n, k_out, dev, dtype, shape),
+         None if v_out is None else _r(n, v_out, dev, dtype, shape), DTYPES.get(dtype, -1), _i(n, err, dev, 1))
 
 
 def lora_kv_gather(pages, block_tokens: int, slots, k_out, v_out=None, err=None, stream=None) -> None:
     """Rows slots[t] of the cache into k_out and v_out [T, kv_heads, head_dim] (either may be None)."""
     n = "lora_kv_gather"
     first = v_out if k_out is None else k_out
+    if first is None:
+        _refuse(n, "k_out or v_out is wanted")
     dev, dst = _device(n, first), first.dtype
-    T, hk, dim = first.shape
-    if k_out is not None and v_out is not None:
-        _same(n, "v_out", v_out.shape, k_out.shape)
-    _run(n, dev, stream, _kv(n, pages, dev, hk, dim, block_tokens), _i(n, slots, dev, T), T, _r(n, k_out, dev, dst, dim),
-         _r(n, v_out, dev, dst, dim), DTYPES.get(dst, -1), _i(n, err, dev, 1))
+    shape = first.shape
+    T, hk, dim = _dims(n, shape)
+    _run(n, dev, stream, _kv(n, pages, dev, hk, dim, block_tokens), _i(n, slots, dev, T), T,
+         None if k_out is None else _r(n, k_out, dev, dst, shape), None if v_out is None else _r(n, v_out, dev, dst, shape),
+         DTYPES.get(dst, -1), _i(n, err, dev, 1))
 
 
 def lora_kv_attend_workspace_size(q_heads: int, kv_heads: int, head_dim: int, max_q_len: int) -> int:
@@ -547,27 +554,28 @@ def lora_kv_attend(q, pages, block_tokens: int, kv_heads: int, block_table, cu_q
     """q, out [T, q_heads, head_dim]; block_table [R, max_blocks], cu_q [R + 1], kv_len [R]."""
     n = "lora_kv_attend"
     dev, dt = _device(n, q), q.dtype
-    T, hq, dim = q.shape
-    _same(n, "out", out.shape, q.shape)
+    shape = q.shape
+    T, hq, dim = _dims(n, shape)
     if block_table.dim() != 2 or ws.get_device() != dev or not ws.is_contiguous():
         _refuse(n, f"block_table is [R, max_blocks], ws contiguous on cuda:{dev}")
     R, width = block_table.shape
-    _run(n, dev, stream, _r(n, q, dev, dt, dim), T, hq, DTYPES.get(dt, -1), _kv(n, pages, dev, kv_heads, dim, block_tokens),
+    _run(n, dev, stream, _r(n, q, dev, dt, shape), T, hq, DTYPES.get(dt, -1), _kv(n, pages, dev, kv_heads, dim, block_tokens),
          _i(n, block_table, dev, R * width), width, _i(n, cu_q, dev, R + 1), _i(n, kv_len, dev, R), R, max_q_len, scale,
-         _r(n, out, dev, dt, dim), _lse(n, lse, q, dev), ws.data_ptr(), ws.numel() * ws.element_size(), _i(n, err, dev, 1))
+         _r(n, out, dev, dt, shape), _lse(n, lse, q, dev), ws.data_ptr(), ws.numel() * ws.element_size(), _i(n, err, dev, 1))
 
 
 def lora_prompt_attend(q, k, v, cu_q, cu_k, scale: float, out, lse=None, err=None, stream=None) -> None:
     """q, out [Tq, q_heads, head_dim], k, v [Tk, kv_heads, head_dim]; cu_q, cu_k [R + 1]."""
     n = "lora_prompt_attend"
     dev, dt = _device(n, q), q.dtype
-    T, hq, dim = q.shape
-    _same(n, "out", out.shape, q.shape)
-    _same(n, "v", v.shape, k.shape)
+    shape, kshape = q.shape, k.shape
+    T, hq, dim = _dims(n, shape)
+    Tk, hk, dk = _dims(n, kshape)
     R = cu_q.numel() - 1
-    _same(n, "cu_k", cu_k.numel(), R + 1)
-    _run(n, dev, stream, _r(n, q, dev, dt, dim), _r(n, k, dev, dt, dim), _r(n, v, dev, dt, dim), T, k.shape[0], hq, k.shape[1],
-         dim, DTYPES.get(dt, -1), _i(n, cu_q, dev, 1), _i(n, cu_k, dev, 1), R, scale, _r(n, out, dev, dt, dim),
+    if dk != dim or cu_k.numel() != R + 1:
+        _refuse(n, f"k has the head_dim of q, cu_k the length of cu_q: {dk} against {dim}, {cu_k.numel()} against {R + 1}")
+    _run(n, dev, stream, _r(n, q, dev, dt, shape), _r(n, k, dev, dt, kshape), _r(n, v, dev, dt, kshape), T, Tk, hq, hk, dim,
+         DTYPES.get(dt, -1), _i(n, cu_q, dev, 1), _i(n, cu_k, dev, 1), R, scale, _r(n, out, dev, dt, shape),
          _lse(n, lse, q, dev), _i(n, err, dev, 1))
 
 

@@ -268,3 +268,44 @@ def test_a_cache_without_pages_in_reserve(H):
     H.lora_kv_layout(i32([0]), i32([3]), None, 16, table, i32([]), None, cu, kl, pos, slots, err=err)
     torch.cuda.synchronize()
     assert int(err.item()) == H.DEV_ERR_NO_PAGES and table.tolist() == [[5, 5]] and kl.tolist() == [0] and slots.tolist() == [-1] * 4
+
+
+def test_the_binding_refuses_tensors_that_do_not_fit(H):
+    """Every check of the binding, on tensors of the device: nothing runs."""
+    z = lambda *n, dtype=BF: torch.zeros(n, dtype=dtype, device="cuda")  # noqa: E731
+    q, k, pos, f = z(4, 8, 64), z(4, 2, 64), i32([0] * 4), z(32, dtype=torch.float32)
+    pages = z(6, H.lora_kv_block_bytes(2, 64, 16), dtype=torch.uint8)
+    slots, table, cu, lens = i32([-1] * 4), i32([[0, 1]]), i32([0, 1]), i32([1])
+    ws = z(H.lora_kv_attend_workspace_size(8, 2, 64, 1), dtype=torch.uint8)
+    ok = {
+        "rope": (lambda **a: H.lora_rope(**a), dict(q=q, k=k, positions=pos, inv_freq=f, q_out=z(4, 8, 64), k_out=z(4, 2, 64))),
+        "append": (lambda **a: H.lora_kv_append(**a), dict(q=q, k=k, v=z(4, 2, 64), positions=pos, inv_freq=f, slots=slots, pages=pages,
+                                                           block_tokens=16, q_out=z(4, 8, 64), k_out=z(4, 2, 64), v_out=z(4, 2, 64))),
+        "gather": (lambda **a: H.lora_kv_gather(**a), dict(pages=pages, block_tokens=16, slots=slots, k_out=z(4, 2, 64), v_out=z(4, 2, 64))),
+        "attend": (lambda **a: H.lora_kv_attend(**a), dict(q=q, pages=pages, block_tokens=16, kv_heads=2, block_table=table, cu_q=cu,
+                                                           kv_len=lens, max_q_len=1, scale=1.0, out=z(4, 8, 64), ws=ws)),
+        "prompt": (lambda **a: H.lora_prompt_attend(**a), dict(q=q, k=k, v=z(4, 2, 64), cu_q=cu, cu_k=cu, scale=1.0, out=z(4, 8, 64))),
+    }
+    for call, args in ok.values():
+        call(**args)
+    torch.cuda.synchronize()
+    wide = z(4, 8, 128)
+    for name, arg, bad in [
+            ("rope", "q", q[0]), ("rope", "k", None), ("rope", "k_out", None), ("rope", "k", z(3, 2, 64)), ("rope", "k", z(4, 2, 32)),
+            ("rope", "q_out", z(4, 8, 32)), ("rope", "q_out", q.float()), ("rope", "positions", i32([0] * 3)), ("rope", "positions", pos.long()),
+            ("rope", "inv_freq", f.double()), ("rope", "q", wide[:, :, ::2]), ("rope", "q", q.cpu()), ("rope", "k", k.cpu()),
+            ("append", "q", z(5, 8, 64)), ("append", "q_out", None), ("append", "v", z(4, 3, 64)), ("append", "k", k[0]),
+            ("append", "k_out", z(4, 2, 64, dtype=torch.float16)), ("append", "slots", i32([0] * 3)), ("append", "pages", pages[:, :64]),
+            ("gather", "k_out", z(3, 2, 64)), ("gather", "v_out", z(4, 2, 64, dtype=torch.float16)), ("gather", "slots", i32([0])),
+            ("attend", "out", z(4, 8, 64, dtype=torch.float16)), ("attend", "out", z(3, 8, 64)), ("attend", "cu_q", i32([0])),
+            ("attend", "kv_len", i32([])), ("attend", "block_table", i32([0, 1])), ("attend", "ws", ws[:-1]), ("attend", "ws", ws.cpu()),
+            ("attend", "q", q[0]), ("attend", "kv_heads", 3),
+            ("prompt", "k", z(4, 2, 32)), ("prompt", "v", z(5, 2, 64)), ("prompt", "cu_k", i32([0])), ("prompt", "out", z(4, 4, 64)),
+            ("prompt", "q", q.float()), ("prompt", "scale", -1.0)]:
+        call, args = ok[name]
+        with pytest.raises(H.LoraError):
+            call(**{**args, arg: bad})
+    with pytest.raises(H.LoraError):
+        H.lora_kv_gather(pages, 16, slots, None)
+    with pytest.raises(H.LoraError):          # the lengths of the last step are not updated in place
+        H.lora_kv_layout(lens, i32([1]), None, 16, table, None, None, cu, lens, pos, slots)
