@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attend_kernel(At
         float qs[NT][NG][2], start[NT][NG][2], cq[NT][2], jump[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float scale = 1.f;   // 2^-qx
+            float scale = 1.f, back = 1.f;   // 2^-qx, 2^qx
             {
                 float top = 0.f;
 #pragma unroll
@@ -408,7 +408,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attend_kernel(At
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
                 // the largest element goes to [2^13, 2^14): odd ones are divided by 16, sums of products stay far from fp32's ends
                 const uint32_t e = __float_as_uint(top) >> 23;
-                if (e != 0 && e != 255) scale = __uint_as_float(min(267u - e, 254u) << 23);
+                if (e != 0 && e != 255) {
+                    const uint32_t to = min(267u - e, 253u);
+                    scale = __uint_as_float(to << 23);
+                    back = __uint_as_float((254u - to) << 23);
+                }
+                if (a.scale < 0.f) scale = -scale;
             }
 #pragma unroll
             for (int ng = 0; ng < NG; ++ng) {
@@ -420,7 +425,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attend_kernel(At
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         x[j] = (float)e[j] * scale;
-                        if (a.scale < 0.f) x[j] = -x[j];
                         if (j & 1) {
                             odd += x[j];
                             x[j] *= 0.0625f;
@@ -448,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attend_kernel(At
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                cq[nt][e] = c / __shfl_sync(~0u, scale, 8 * t4 + 4 * e);
-                jump[nt][e] = kJump / cq[nt][e];
+                cq[nt][e] = c * __shfl_sync(~0u, back, 8 * t4 + 4 * e);
+                jump[nt][e] = __fdividef(kJump, cq[nt][e]);   // where it lies exactly does not matter
             }
         }
         // Last key each of the thread's columns sees, and the least of the tile.
@@ -568,9 +572,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attend_kernel(At
                 if (top > sref) {
                     // the next power of two above (steps that are not finite only reach the columns that see them)
                     const float n = __uint_as_float((__float_as_uint(top) & 0x7f800000u) + 0x00800000u);
-                    ratio = sref / n;
+                    const float inv = __uint_as_float(0x7f000000u - __float_as_uint(n));   // 1 / n: n lies within 2^-23 and 2^16
+                    ratio = sref * inv;
                     sref = n;
-                    rs = (float)(1 << kShift) / n;
+                    rs = (float)(1 << kShift) * inv;
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
