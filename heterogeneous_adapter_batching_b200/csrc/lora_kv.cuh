@@ -88,6 +88,8 @@ struct AttendArgs {
     float *lse;
     void *ws;
     int32_t *err;
+    int group;              // q heads of a kv head
+    uint32_t inv_group;     // 65536 / group + 1
 };
 size_t attend_workspace(int hq, int hkv, int dim, int max_q);
 int launch_kv_attend(const AttendArgs &a, cudaStream_t st);

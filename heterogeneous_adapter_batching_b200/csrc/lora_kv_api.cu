@@ -185,8 +185,9 @@ int lora_kv_attend(const lora_rows_t *q, int T, int q_heads, int dtype, const lo
     if (T == 0) return LORA_OK;
     if ((long long)T * (q_heads / kv->kv_heads) > INT32_MAX) return LORA_ERR_TOO_LARGE;
     if (!rows_ok(q, q_heads, dtype) || !out_ok(out, T, q_heads, kv->head_dim, dtype)) return LORA_ERR_INVALID_ARG;
+    const int group = q_heads / kv->kv_heads;
     const AttendArgs a{rows(q), rows(out), T, q_heads, kv->head_dim, dtype, cache(kv), block_table, max_blocks, cu_q,
-                       kv_len, R, max_q_len, scale, lse, ws, err_dev};
+                       kv_len, R, max_q_len, scale, lse, ws, err_dev, group, 65536u / (uint32_t)group + 1};
     return launch_kv_attend(a, reinterpret_cast<cudaStream_t>(stream));
 }
 

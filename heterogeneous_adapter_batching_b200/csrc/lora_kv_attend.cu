@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attend_kernel(At
     extern __shared__ unsigned char smem_raw[];
     Smem<DIM, NT, U> &sm = *reinterpret_cast<Smem<DIM, NT, U> *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-    const int G = a.hq / a.c.heads;
+    const int G = a.group;
 
     // Units of the batch and this CTA's range of them.
     const int per = (a.R + kThreads - 1) / kThreads, ra = min(a.R, tid * per), rb = min(a.R, ra + per);
@@ -305,19 +305,29 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attend_kernel(At
     comp.start(a, G, sm.first, u0 - sm.base, u1 - u0);
     if (comp.n == 0 && !comp.next(a, G)) return;
     load = comp;
+    // Columns of a tile as (row, head): the tile's first row and the columns of that row before it, once per piece; then a product
+    // in place of each division by G (exact: x < LORA_KV_MAX_GROUP + NC).
+    const auto by_g = [&](int x) { return (int)((uint32_t)x * a.inv_group >> 16); };
+    const auto first_row = [&](int ct, int &rest) {
+        const int row = ct == 0 ? 0 : ct * NC / G;
+        rest = ct * NC - row * G;
+        return row;
+    };
     // Queries of a piece, asked for before they are needed: behind the prologue's table and cache loads, or the join.
     uint4 raw[NT][NG][2];
     const auto load_queries = [&]() {
+        int rest;
+        const int row0 = first_row(comp.ct, rest);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int gc = comp.ct * NC + nt * 8 + g, qi = gc / G, head = comp.h * G + gc - qi * G;
+            const int x = rest + nt * 8 + g, over = by_g(x), qi = row0 + over, head = comp.h * G + x - over * G;
             const H *row = reinterpret_cast<const H *>(a.q.p) + (long long)(comp.q.q0 + qi) * a.q.ts + (long long)head * a.q.hs;
 #pragma unroll
             for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     raw[nt][ng][i] = make_uint4(0, 0, 0, 0);
-                    if (gc < comp.q.nq * G) raw[nt][ng][i] = *reinterpret_cast<const uint4 *>(row + 64 * ng + 16 * t4 + 8 * i);
+                    if (qi < comp.q.nq) raw[nt][ng][i] = *reinterpret_cast<const uint4 *>(row + 64 * ng + 16 * t4 + 8 * i);
                 }
         }
     };
@@ -458,11 +468,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attend_kernel(At
         }
         // Last key each of the thread's columns sees, and the least of the tile.
         int lim[NT][2];
-        const int back = comp.q.len - comp.q.nq, least = back + comp.ct * NC / G;
+        int rest;
+        const int row0 = first_row(comp.ct, rest), back = comp.q.len - comp.q.nq, least = back + row0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) lim[nt][e] = back + min(comp.q.nq - 1, (comp.ct * NC + nt * 8 + 2 * t4 + e) / G);
+            for (int e = 0; e < 2; ++e) lim[nt][e] = back + min(comp.q.nq - 1, row0 + by_g(rest + nt * 8 + 2 * t4 + e));
 
         float o[NT][NG][4][4] = {}, om[NT][NG][2] = {}, l[NT][2] = {};
         float m[NT][2], mc[NT][2], thr[NT][2];   // reference score (-inf: none yet); it times c (0); the score that moves it
@@ -473,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attend_kernel(At
                 m[nt][e] = thr[nt][e] = -INFINITY;
                 mc[nt][e] = 0.f;
             }
+        bool begun = false;
         float sref = 0.f, rs = 0.f;   // largest step so far as a power of two; 2^kShift over it
 
         // U granules at `st`, the first of them granule gi of the request. EDGE: some are missing (`bits`) or hold masked tokens.
@@ -592,6 +604,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attend_kernel(At
                         m[nt][e] = n;
                         mc[nt][e] = n == -INFINITY ? 0.f : n * cq[nt][e];
                         thr[nt][e] = n + jump[nt][e];
+                        if (!begun) continue;   // nothing to scale yet
                         l[nt][e] *= f;
 #pragma unroll
                         for (int ng = 0; ng < NG; ++ng) {
@@ -656,6 +669,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attend_kernel(At
                     }
                 }
             }
+            begun = true;
         };
 
         const int gend = comp.g1();
@@ -739,9 +753,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attend_kernel(At
                 }
                 continue;
             }
-            const int gc = cur.ct * NC + col;
-            if (gc >= cur.q.nq * G) continue;
-            const int qi = gc / G, head = cur.h * G + gc - qi * G;
+            const int x0 = rest + col, over = by_g(x0), qi = row0 + over, head = cur.h * G + x0 - over * G;
+            if (qi >= cur.q.nq) continue;
             const float inv = ll == 0.f ? 0.f : 1.f / ll;
             uint4 u;
             H *e = reinterpret_cast<H *>(&u);
@@ -778,7 +791,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, con
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Split s = split[blockIdx.x];
     if (s.last == 0) return;
-    const int G = a.hq / a.c.heads, first = blockIdx.x, n = s.last - first + 1;
+    const int G = a.group, first = blockIdx.x, n = s.last - first + 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int cols = s.cols, W = kJoinWarps / cols;   // W: warps of a column
     const int col = warp % cols, w = warp / cols;
