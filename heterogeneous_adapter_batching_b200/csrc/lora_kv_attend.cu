@@ -44,14 +44,14 @@
 // saved nothing: 25.4 against 23.1 us for one request, 54.5 against 47.9 us for
 // 48 requests of up to 4 tokens, as the main loop spills more registers.)
 //
-// Measured, 32 / 8 heads of 128, bf16: 32 requests of 8192 tokens 78 us, 3.9 TB/s
-// or 59 % of a copy's rate; 128 requests of 1 to 16384 tokens 64 us (47 %); one of
+// Measured, 32 / 8 heads of 128, bf16: 32 requests of 8192 tokens 77 us, 3.9 TB/s
+// or 60 % of a copy's rate; 128 requests of 1 to 16384 tokens 62 us (48 %); one of
 // 32749 tokens 23 us.  It is bound by issue slots and latency at 12 warps an SM:
 // 342 instructions a granule and warp, of which 64 products; memory would allow
 // 46 us.  Two granules a warp and step at 3 CTAs an SM: one granule at 4 CTAs takes
 // 86 to 90 us, four at 2 CTAs 75 us but 1.5 times as long for short requests.
-// Short requests cost their pieces' beginning and end, about 5 us each and CTA
-// (1024 requests of 64 tokens: 92 us).
+// Short requests cost their pieces' beginning and end, about 4 us each and CTA
+// (1024 requests of 64 tokens: 79 us).
 #include <type_traits>
 
 #include "lora_internal.cuh"
@@ -64,7 +64,7 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kMaxCtas = 444;                      // one column tile: 3 CTAs on each of 148 SMs; two: 2
 constexpr int kStages = 3;
-constexpr int kFixed = 2;                          // units that starting and joining a segment costs beside its rounds
+constexpr int kFixed = 2;                          // units that starting and joining a segment costs beside its rounds (1: 67, 3: 66, 2: 62 us, ragged)
 constexpr float kJump = 10.f;                      // log2 by which a score may exceed the reference
 constexpr int kShift = 5;                          // weights are scaled by 2^kShift in fp16
 constexpr int kJoinThreads = 512;
@@ -844,6 +844,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, con
     if (a.lse && lane == 0) a.lse[(size_t)(s.q0 + qi) * a.hq + head] = ll == 0.f ? -INFINITY : 0.6931471805599453f * (ref + log2f(ll));
 }
 
+// Two column tiles that share one reading of the cache, or one at a time: up to 8 columns there is only one.  Above, two take 110
+// against 116 us (32 requests of 8192, 4 tokens of 4 heads) and 38 against 45 us (16 heads on one), though 43.7 against 41.7 us
+// for 48 ragged requests of up to 4096.
 int tiles_of(int hq, int hkv, int max_q) { return (long long)max_q * (hq / hkv) <= 8 ? 1 : 2; }
 template <int NT>
 constexpr int ctas_per_sm() { return NT == 1 ? 3 : 2; }   // what the registers allow
