@@ -35,9 +35,13 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[dict
     if scaling is None:
         return f.float(), 1.0
     kind, s = scaling["kind"], float(scaling["factor"])
+    if not 0.0 < s < math.inf:
+        raise ValueError("factor is a positive number")
     if kind == "linear":
         return (f / s).float(), 1.0
     if kind == "ntk":
+        if rot_dim == 2:
+            raise ValueError("one pair has no slowest one beside the fastest")
         return ((base * s ** (rot_dim / (rot_dim - 2))) ** (-i / rot_dim)).float(), 1.0
     n = float(scaling["original_max_position"])
     if kind == "yarn":
@@ -49,6 +53,8 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[dict
         return (f * (1 - ramp) + f / s * ramp).float(), 0.1 * math.log(s) + 1.0 if s > 1 else 1.0
     if kind == "bands":
         low, high = scaling.get("low_freq_factor", 1.0), scaling.get("high_freq_factor", 4.0)
+        if not low < high:
+            raise ValueError("low_freq_factor lies below high_freq_factor")
         keep = ((n * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
         return (f * keep + f / s * (1 - keep)).float(), 1.0
     raise ValueError(f"unknown scaling {kind!r}")

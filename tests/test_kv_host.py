@@ -239,3 +239,13 @@ def test_rope_frequencies():
         rf(63)
     with pytest.raises(ValueError):
         rf(64, scaling={"kind": "other", "factor": 2.0, "original_max_position": 1})
+
+
+@pytest.mark.parametrize("rot_dim,scaling", [(0, None), (64, {"kind": "linear", "factor": 0.0}), (64, {"kind": "linear", "factor": -2.0}),
+                                             (64, {"kind": "ntk", "factor": float("nan")}), (2, {"kind": "ntk", "factor": 2.0}),
+                                             (64, {"kind": "bands", "factor": 2.0, "original_max_position": 64, "low_freq_factor": 4.0}),
+                                             (64, {"kind": "yarn", "factor": float("inf"), "original_max_position": 64})])
+def test_rope_frequencies_refusals(rot_dim, scaling):
+    from heterogeneous_adapter_batching_b200 import rope_frequencies as rf
+    with pytest.raises(ValueError):
+        rf(rot_dim, scaling=scaling)
