@@ -382,6 +382,8 @@ class SlotCache:
 
 # The calls below run once per layer and step, some of them for a few microseconds: their checks are plain attribute
 # comparisons, pointers go as integers and row tensors as packed lora_rows_t.
+_I32 = torch.int32
+_raw_stream, _current_device = (getattr(torch._C, x, None) for x in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
 _ROWS = struct.Struct("=Qqq")                 # lora_rows_t
 _KV = struct.Struct("=QQiiii")                # lora_kv_cache_t
 
@@ -418,7 +420,7 @@ def _i(name: str, t: Optional[torch.Tensor], dev: int, n: int):
     """Address of a contiguous int32 tensor of at least n elements (None: a null pointer)."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
+    if t.dtype is not _I32 or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
         _refuse(name, f"index arrays are contiguous int32 tensors on cuda:{dev} with at least {n} elements")
     return t.data_ptr()
 
@@ -451,8 +453,8 @@ def _lse(name, lse, q, dev):
 def _run(name: str, dev: int, stream, *args) -> None:
     """Call `name` with the tensors' device current, on `stream` (None: that device's current stream)."""
     fn = getattr(_lib or load_library(), name)
-    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
-    if torch._C._cuda_getDevice() == dev:
+    st = _raw_stream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
+    if _current_device() == dev:
         rc = fn(*args, st)
     else:
         with torch.cuda.device(dev):
