@@ -14,8 +14,11 @@
 // fp16((max x - min x) / 15), code = clamp(round_even((x - low) / step), 0, 15).
 // The quotient is formed in 32 bits; where it lies within 2^-17 of a border
 // between two codes (its error is below 15.5 * 3 * 2^-24) the side is decided by
-// the sign of (x - low) - step * (border) in 64 bits, which is exact.  That
-// happens to one warp in a hundred.
+// the sign of (x - low) - step * (border) in 64 bits; a difference of which 64
+// bits hold only a part comes with the rest.  That happens to one warp in a
+// hundred.  The span, its fifteenth and the rounding to fp16 go through 64 bits:
+// a quotient that 64 bits do not hold is rounded to odd there (its last bit says
+// that more follows), which makes the rounding to fp16 the only one.
 //
 // Layout of the work: a head is dim / 16 chunks of 16 elements, one thread per
 // chunk: elements [8 c, 8 c + 8) and [rot / 2 + 8 c, + 8) in the half layout,
@@ -112,6 +115,23 @@ __device__ __forceinline__ uint32_t range_of(const uint32_t (&u)[4]) {
     return Pair<D>::less(__byte_perm(l, g, 0x5410), __byte_perm(l, g, 0x7632));
 }
 
+// x - y rounded, and what the rounding left out.
+__device__ __forceinline__ double minus(double x, double y, double &rest) {
+    const double d = x - y, b = d - x;
+    rest = (x - (d - b)) - (y + b);
+    return d;
+}
+// (x - y) / 15 rounded once to fp16.
+__device__ __forceinline__ __half fifteenth(double x, double y) {
+    double rest;
+    const double diff = minus(x, y, rest);
+    // a neighbour of the quotient: a first value, and its remainder times the reciprocal
+    const double first = diff * (1.0 / 15.0), quot = fma(fma(-15.0, first, diff), 1.0 / 15.0, first);
+    const double more = fma(-15.0, quot, diff) + rest;   // 15 (exact - quot)
+    const long long bits = __double_as_longlong(quot);
+    return __double2half(__longlong_as_double(more > 0.0 ? bits | 1 : more < 0.0 ? (bits - 1) | 1 : bits));
+}
+
 // Codes of eight elements for (step, low), inv = 1 / step or 0 (see the head of the file).
 template <class D>
 __device__ __forceinline__ uint32_t codes_of(const uint32_t (&u)[4], float low, float step, float inv) {
@@ -135,7 +155,10 @@ __device__ __forceinline__ uint32_t codes_of(const uint32_t (&u)[4], float low, 
             const float x = i & 1 ? v.y : v.x, t = fminf(fmaxf((x - low) * inv, 0.f), 15.f), k = floorf(t);
             float n = rintf(t);
             if (fabsf(t - k - 0.5f) < 0x1p-16f) {
-                const double side = fma(-(double)step, (double)k + 0.5, (double)x - (double)low);
+                double rest;
+                const double diff = minus((double)x, (double)low, rest);
+                double side = fma(-(double)step, (double)k + 0.5, diff);   // zero, or far above the rest
+                if (side == 0.0) side = rest;
                 n = k + (side > 0.0 || (side == 0.0 && ((int)k & 1)) ? 1.f : 0.f);
             }
             w = (w << 4) | (uint32_t)n;
@@ -273,10 +296,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tok_per_
             uint32_t r = Pair<D>::less(g0 == g ? rx : Pair<D>::kInf, g1 == g ? ry : Pair<D>::kInf);
             for (int d = 1; d < chunks; d <<= 1) r = Pair<D>::less(r, __shfl_xor_sync(mask, r, d));
             const float2 e = Pair<D>::get(r);   // least, minus the greatest
-            // the quotient by 15 rounded correctly: a first value, and its remainder times the reciprocal
-            const double diff = -(double)e.y - (double)e.x, first = diff * (1.0 / 15.0);
-            const double quot = fma(fma(-15.0, first, diff), 1.0 / 15.0, first);
-            const __half hl = __float2half_rn(e.x), hs = __float2half_rn((float)quot);
+            const __half hl = __float2half_rn(e.x), hs = fifteenth(-(double)e.y, (double)e.x);
             if (c == 0)
                 reinterpret_cast<__half2 *>(base + kv_code_bytes(a.dim))[(off % LORA_KV_GRANULE) * (a.dim / LORA_KV_GROUP) + g] =
                     __halves2half2(hs, hl);
