@@ -12,6 +12,8 @@
 //
 // Quantisation of 64 dimensions x of one head: low = fp16(min x), step =
 // fp16((max x - min x) / 15), code = clamp(round_even((x - low) / step), 0, 15).
+// A low that is infinite comes with a NaN as step: n * step + low would be that
+// infinity, which attention drops as a key of weight zero.
 // The quotient is formed in 32 bits; where it lies within 2^-17 of a border
 // between two codes (its error is below 15.5 * 3 * 2^-24) the side is decided by
 // the sign of (x - low) - step * (border) in 64 bits; a difference of which 64
@@ -296,7 +298,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tok_per_
             uint32_t r = Pair<D>::less(g0 == g ? rx : Pair<D>::kInf, g1 == g ? ry : Pair<D>::kInf);
             for (int d = 1; d < chunks; d <<= 1) r = Pair<D>::less(r, __shfl_xor_sync(mask, r, d));
             const float2 e = Pair<D>::get(r);   // least, minus the greatest
-            const __half hl = __float2half_rn(e.x), hs = fifteenth(-(double)e.y, (double)e.x);
+            const __half hl = __float2half_rn(e.x);
+            __half hs = fifteenth(-(double)e.y, (double)e.x);
+            if (__hisinf(hl)) hs = __ushort_as_half(0x7fff);   // no sum with an infinite low is a value: NaN
             if (c == 0)
                 reinterpret_cast<__half2 *>(base + kv_code_bytes(a.dim))[(off % LORA_KV_GRANULE) * (a.dim / LORA_KV_GROUP) + g] =
                     __halves2half2(hs, hl);

@@ -509,7 +509,7 @@ int lora_rope(const lora_rows_t *q, int q_heads, const lora_rows_t *k, int k_hea
  *     low = fp16(min), step = fp16((max - min) / 15),
  *     code = clamp(round_even((x - low) / step), 0, 15)      (0 when step = 0)
  * with every rounding taken from the exact value.  A group that holds a NaN or
- * an infinity, or spans more than fp16 reaches, reads back as NaN.
+ * an infinity, or whose low or step lies beyond fp16's range, reads back as NaN.
  *   v [T][kv_heads] rows of src_dtype; k_out and v_out (the rounded keys and
  *   values, for lora_prompt_attend) may be NULL; q may be NULL with q_heads 0.
  * The slots of a call are distinct.  A slot beyond the cache is skipped and

@@ -101,3 +101,30 @@ def test_codes_beside_a_border(H):
     check(H, [spread(-1.0, 29.0, tiny), spread(-3.0, 27.0, tiny), spread(-5.0, 25.0, tiny), spread(-29.0, 1.0, tiny)], BF)
     tiny = [0.0, 2.0 ** -24, -2.0 ** -24, 2.0 ** -14, -2.0 ** -14]
     check(H, [spread(-1.0, 29.0, tiny), spread(-3.0, 27.0, tiny)], FP)
+
+
+@pytest.mark.parametrize("lo,hi", [(-1e5, 0.0), (-1e5, -0.9e5), (-65536.0, 3.0), (-3e38, -3e38), (66048.0, 66048.0), (1e5, 1.2e5), (7e4, 3e38), (-1e6, 1e6)])
+def test_groups_beyond_fp16_read_back_as_nan(H, lo, hi):
+    """A least value or a step that fp16 does not hold makes its group NaN, and no other."""
+    good = spread(-65280.0, 65280.0)                         # the widest least value that bf16 rows have within fp16's range
+    cache, kb, vb = cached(H, torch.stack([good, spread(lo, hi).clamp(lo, hi), good]), BF)
+    for back in (kb, vb):
+        assert torch.isnan(back[1]).all() and torch.isfinite(back[0]).all() and torch.isfinite(back[2]).all()
+
+
+def test_a_greatest_value_beyond_fp16_is_fine(H):
+    """Codes reach above fp16's range as long as the least value and the step lie within it."""
+    check(H, [spread(-6e4, 1e5), spread(0.0, 9e5)], BF)
+
+
+def test_a_key_beyond_fp16_is_not_dropped(H):
+    """Such a key shows as NaN in the attention that sees it; a score of minus infinity would leave it out without a word."""
+    q = torch.ones((2, 2, 64), dtype=BF, device="cuda")
+    k, v = (torch.randn((3, 1, 64), dtype=BF, device="cuda") for _ in range(2))
+    k[2] = spread(-1e5, -0.9e5).to(BF).cuda()
+    pages = torch.zeros((2, K.block_bytes(1, 64, 16)), dtype=torch.uint8, device="cuda")
+    H.lora_kv_append(None, k, v, i32([0, 1, 2]), None, i32([0, 1, 2]), pages, 16, None)
+    out = torch.empty_like(q)
+    ws = torch.empty(H.lora_kv_attend_workspace_size(2, 1, 64, 2), dtype=torch.uint8, device="cuda")
+    H.lora_kv_attend(q, pages, 16, 1, i32([[0]]), i32([0, 2]), i32([3]), 2, 0.125, out, ws)
+    assert torch.isfinite(out[0].float()).all() and torch.isnan(out[1].float()).all()
