@@ -57,7 +57,7 @@ EXPORTS = [
     "lora_apply_multi", "lora_apply_multi_planned",
     "lora_slot_cache_create", "lora_slot_cache_destroy", "lora_slot_cache_acquire", "lora_slot_cache_unpin",
     "lora_slot_cache_invalidate", "lora_slot_cache_lookup", "lora_slot_cache_stats",
-    "lora_kv_block_bytes", "lora_kv_layout", "lora_rope", "lora_kv_append", "lora_kv_gather",
+    "lora_kv_block_bytes", "lora_kv_layout", "lora_kv_layout_held", "lora_rope", "lora_kv_append", "lora_kv_gather",
     "lora_kv_attend_workspace_size", "lora_kv_attend", "lora_prompt_attend",
     "lora_set_option", "lora_get_option", "lora_last_cuda_error", "lora_last_launch_count",
 ]
@@ -134,6 +134,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                       ctypes.POINTER(ctypes.c_int64)]),
         "lora_kv_block_bytes": (Z, [I, I, I]),
         "lora_kv_layout": (I, [V, V, V, I, I, I, V, I, V, I, V, V, V, V, V, V, V, V, V]),
+        "lora_kv_layout_held": (I, [V, V, V, I, I, I, V, I, V, I, V, V, V, V, V, V, V, V, V, V, V]),
         "lora_rope": (I, [V, I, V, I, I, I, I, V, V, I, I, ctypes.c_double, V, V, I, V]),
         "lora_kv_append": (I, [V, I, V, V, I, I, V, V, I, I, ctypes.c_double, V, V, V, V, V, I, V, V]),
         "lora_kv_gather": (I, [V, V, I, V, V, I, V, V]),
@@ -468,21 +469,25 @@ def lora_kv_block_bytes(kv_heads: int, head_dim: int, block_tokens: int) -> int:
 
 
 def lora_kv_layout(past_len, new_len, req_ids, block_tokens: int, block_table, free_pages, free_head, cu_new, kv_len,
-                   positions, slots, ids=None, free_head_out=None, err=None, stream=None) -> None:
+                   positions, slots, ids=None, free_head_out=None, err=None, stream=None, held=None, held_out=None) -> None:
     """past_len, new_len, req_ids [R], block_table [R, max_blocks]; cu_new [R + 1], kv_len [R], positions, slots, ids [T]
-    out; free_pages None: block_table already names every block."""
+    out; free_pages None: block_table already names every block.  held, held_out [R]: lora_kv_layout_held."""
     n = "lora_kv_layout"
     dev = _device(n, past_len)
     if block_table.dim() != 2 or positions.dim() != 1:
         _refuse(n, "block_table is [R, max_blocks], positions [T]")
+    if (held is None) != (held_out is None):
+        _refuse(n, "held and held_out come together")
     R, T, width = past_len.numel(), positions.numel(), block_table.shape[1]
     free = _i(n, free_pages, dev, 0)
     if free == 0:   # an empty list is a list: any address that is not null, nothing is read there
         free = new_len.data_ptr()
-    _run(n, dev, stream, _i(n, past_len, dev, R), _i(n, new_len, dev, R), _i(n, req_ids, dev, R), R, T, block_tokens,
-         _i(n, block_table, dev, R * width), width, free, 0 if free_pages is None else free_pages.numel(),
-         _i(n, free_head, dev, 1), _i(n, cu_new, dev, R + 1), _i(n, kv_len, dev, R), _i(n, positions, dev, T),
-         _i(n, slots, dev, T), _i(n, ids, dev, T), _i(n, free_head_out, dev, 1), _i(n, err, dev, 1))
+    more = () if held is None else (_i(n, held, dev, R), _i(n, held_out, dev, R))
+    _run(n if held is None else "lora_kv_layout_held", dev, stream, _i(n, past_len, dev, R), _i(n, new_len, dev, R),
+         _i(n, req_ids, dev, R), R, T, block_tokens, _i(n, block_table, dev, R * width), width, free,
+         0 if free_pages is None else free_pages.numel(), _i(n, free_head, dev, 1), _i(n, cu_new, dev, R + 1),
+         _i(n, kv_len, dev, R), _i(n, positions, dev, T), _i(n, slots, dev, T), _i(n, ids, dev, T),
+         _i(n, free_head_out, dev, 1), *more, _i(n, err, dev, 1))
 
 
 def lora_rope(q, k, positions, inv_freq, q_out, k_out=None, interleaved: bool = False, mscale: float = 1.0,

@@ -49,6 +49,8 @@ struct LayoutArgs {
     int num_free;
     const int32_t *free_head;
     int32_t *cu, *kv_len, *positions, *slots, *ids, *head_out, *err;
+    const int32_t *held;   // null: a row holds the blocks of its past
+    int32_t *held_out;
 };
 int launch_kv_layout(const LayoutArgs &a, cudaStream_t st);
 

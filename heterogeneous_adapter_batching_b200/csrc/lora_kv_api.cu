@@ -65,6 +65,26 @@ bool rope_ok(int src, int dst, int T, int dim, const int32_t *positions, const f
            rot >= 0 && rot <= dim && rot % 16 == 0 && (rot == 0 || freq) && (T == 0 || positions);
 }
 
+int layout(const LayoutArgs &a, lora_stream_t stream) {
+    reset_launch_count();
+    if (!a.past || !a.fresh_len || !a.table || !a.cu || !a.kv_len || (a.T > 0 && (!a.positions || !a.slots)) || a.R < 1 ||
+        a.T < 0 || a.max_blocks < 1 || a.num_free < 0)
+        return LORA_ERR_INVALID_ARG;
+    if (a.block < 1 || a.block > 1024 || a.block % LORA_KV_GRANULE) return LORA_ERR_INVALID_ARG;
+    if (a.R > LORA_KV_MAX_REQUESTS || ((long long)a.max_blocks + 1) * a.block > INT32_MAX) return LORA_ERR_TOO_LARGE;
+    // Every CTA reads the inputs for itself while others write: a kv_len that is past_len would be read half updated.
+    const Span in[] = {{a.past, a.R}, {a.fresh_len, a.R}, {a.req_ids, a.R}, {a.free_pages, a.num_free}, {a.free_head, 1}, {a.held, a.R}};
+    const Span out[] = {{a.table, (long long)a.R * a.max_blocks}, {a.cu, a.R + 1}, {a.kv_len, a.R}, {a.positions, a.T},
+                        {a.slots, a.T}, {a.ids, a.T}, {a.head_out, 1}, {a.held_out, a.R}};
+    for (const Span &o : out) {
+        for (const Span &i : in)
+            if (overlap(o, i)) return LORA_ERR_INVALID_ARG;
+        for (const Span &i : out)
+            if (&i != &o && overlap(o, i)) return LORA_ERR_INVALID_ARG;
+    }
+    return launch_kv_layout(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -80,25 +100,23 @@ int lora_kv_layout(const int32_t *past_len, const int32_t *new_len, const int32_
                    int block_tokens, int32_t *block_table, int max_blocks, const int32_t *free_pages, int num_free,
                    const int32_t *free_head, int32_t *cu_new, int32_t *kv_len, int32_t *positions, int32_t *slots,
                    int32_t *ids, int32_t *free_head_out, int32_t *err_dev, lora_stream_t stream) {
-    reset_launch_count();
-    if (!past_len || !new_len || !block_table || !cu_new || !kv_len || (T > 0 && (!positions || !slots)) || R < 1 ||
-        T < 0 || max_blocks < 1 || num_free < 0)
+    return layout(LayoutArgs{past_len, new_len, req_ids, R, T, block_tokens, block_table, max_blocks, free_pages, num_free,
+                             free_head, cu_new, kv_len, positions, slots, ids, free_head_out, err_dev, nullptr, nullptr},
+                  stream);
+}
+
+int lora_kv_layout_held(const int32_t *past_len, const int32_t *new_len, const int32_t *req_ids, int R, int T,
+                        int block_tokens, int32_t *block_table, int max_blocks, const int32_t *free_pages, int num_free,
+                        const int32_t *free_head, int32_t *cu_new, int32_t *kv_len, int32_t *positions, int32_t *slots,
+                        int32_t *ids, int32_t *free_head_out, const int32_t *held, int32_t *held_out, int32_t *err_dev,
+                        lora_stream_t stream) {
+    if (!held || !held_out) {
+        reset_launch_count();
         return LORA_ERR_INVALID_ARG;
-    if (block_tokens < 1 || block_tokens > 1024 || block_tokens % LORA_KV_GRANULE) return LORA_ERR_INVALID_ARG;
-    if (R > LORA_KV_MAX_REQUESTS || ((long long)max_blocks + 1) * block_tokens > INT32_MAX) return LORA_ERR_TOO_LARGE;
-    // Every CTA reads the inputs for itself while others write: a kv_len that is past_len would be read half updated.
-    const Span in[] = {{past_len, R}, {new_len, R}, {req_ids, R}, {free_pages, num_free}, {free_head, 1}};
-    const Span out[] = {{block_table, (long long)R * max_blocks}, {cu_new, R + 1}, {kv_len, R}, {positions, T}, {slots, T},
-                        {ids, T}, {free_head_out, 1}};
-    for (const Span &o : out) {
-        for (const Span &i : in)
-            if (overlap(o, i)) return LORA_ERR_INVALID_ARG;
-        for (const Span &i : out)
-            if (&i != &o && overlap(o, i)) return LORA_ERR_INVALID_ARG;
     }
-    const LayoutArgs a{past_len, new_len, req_ids, R, T, block_tokens, block_table, max_blocks, free_pages, num_free,
-                       free_head, cu_new, kv_len, positions, slots, ids, free_head_out, err_dev};
-    return launch_kv_layout(a, reinterpret_cast<cudaStream_t>(stream));
+    return layout(LayoutArgs{past_len, new_len, req_ids, R, T, block_tokens, block_table, max_blocks, free_pages, num_free,
+                             free_head, cu_new, kv_len, positions, slots, ids, free_head_out, err_dev, held, held_out},
+                  stream);
 }
 
 int lora_rope(const lora_rows_t *q, int q_heads, const lora_rows_t *k, int k_heads, int src_dtype, int T, int head_dim,

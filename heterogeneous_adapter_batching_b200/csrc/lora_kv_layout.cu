@@ -2,7 +2,8 @@
 // its requests' lengths.
 //
 // With before_r = ceil(past_r / b) and after_r = ceil((past_r + new_r) / b), a
-// request takes after_r - before_r pages; rows and pages are handed out by two
+// request takes after_r - before_r pages (less those that its row holds beyond
+// before_r, where the caller says how many it holds); rows and pages are handed out by two
 // prefix sums over the requests.  Row t belongs to the request whose row range
 // holds it (a binary search in the sums), its token to block pos / b of that
 // request: a page of the free list if that block is new, else an entry of the
@@ -27,15 +28,26 @@ struct Sums {
 
 struct Need {
     int rows, pages;   // rows the request brings, pages it takes
+    int after;         // blocks it has afterwards
     bool bad;          // its lengths are refused
 };
 
-__device__ __forceinline__ Need need_of(const LayoutArgs &a, int past, int fresh) {
+// Blocks of a request that are there before the call; the next one takes the first of its pages.
+__device__ __forceinline__ int blocks_before(const LayoutArgs &a, int r, int past) {
+    const int n = (past + a.block - 1) / a.block;
+    return a.held ? max(n, a.held[r]) : n;
+}
+
+__device__ __forceinline__ Need need_of(const LayoutArgs &a, int r, int past, int fresh) {
     Need n;
     n.rows = fresh < 0 ? 0 : fresh;
-    n.bad = past < 0 || fresh < 0 || (long long)past + fresh > (long long)a.max_blocks * a.block;
-    n.pages = 0;
-    if (!n.bad && a.free_pages) n.pages = (past + fresh + a.block - 1) / a.block - (past + a.block - 1) / a.block;
+    n.bad = past < 0 || fresh < 0 || (long long)past + fresh > (long long)a.max_blocks * a.block ||
+            (a.held && (a.held[r] < 0 || a.held[r] > a.max_blocks));
+    n.pages = n.after = 0;
+    if (n.bad) return n;
+    const int before = blocks_before(a, r, past);
+    n.after = max(before, (past + fresh + a.block - 1) / a.block);
+    if (a.free_pages) n.pages = n.after - before;
     return n;
 }
 
@@ -62,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) kv_layout_kernel(LayoutArgs a) {
 
     Sums mine{0, 0};
     for (int r = r0; r < r1; ++r) {
-        const Need n = need_of(a, a.past[r], a.fresh_len[r]);
+        const Need n = need_of(a, r, a.past[r], a.fresh_len[r]);
         mine.rows += n.rows;
         mine.pages += n.pages;
     }
@@ -87,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) kv_layout_kernel(LayoutArgs a) {
     int flags = head < 0 || head > a.num_free ? LORA_DEV_ERR_NO_PAGES : 0;
     for (int r = r0; r < r1; ++r) {
         const int past = a.past[r], fresh = a.fresh_len[r];
-        const Need n = need_of(a, past, fresh);
+        const Need n = need_of(a, r, past, fresh);
         run.rows += n.rows;
         run.pages += n.pages;
         bool f = n.bad || (n.rows > 0 && run.rows > a.T);
@@ -104,6 +116,7 @@ __global__ void __launch_bounds__(kThreads) kv_layout_kernel(LayoutArgs a) {
             if (r == 0) a.cu[0] = 0;
             a.cu[r + 1] = row_end[r];
             a.kv_len[r] = f ? 0 : past + fresh;
+            if (a.held_out) a.held_out[r] = f ? a.held[r] : n.after;
         }
     }
     __syncthreads();
@@ -117,14 +130,14 @@ __global__ void __launch_bounds__(kThreads) kv_layout_kernel(LayoutArgs a) {
         const int r = owner(page_end, a.R, j);
         if (failed[r]) continue;
         const int start = r ? page_end[r - 1] : 0;
-        a.table[(size_t)r * a.max_blocks + (a.past[r] + a.block - 1) / a.block + j - start] = a.free_pages[head + j];
+        a.table[(size_t)r * a.max_blocks + blocks_before(a, r, a.past[r]) + j - start] = a.free_pages[head + j];
     }
     const int used = row_end[a.R - 1];
     for (int t = me; t < a.T; t += all) {
         int pos = -1, slot = -1, id = -1;
         const int r = t < used ? owner(row_end, a.R, t) : 0;
         if (t < used && !failed[r]) {
-            const int past = a.past[r], before = (past + a.block - 1) / a.block;
+            const int past = a.past[r], before = blocks_before(a, r, past);
             pos = past + t - (r ? row_end[r - 1] : 0);
             const int blk = pos / a.block;
             const int page = a.free_pages && blk >= before ? a.free_pages[head + (r ? page_end[r - 1] : 0) + blk - before]

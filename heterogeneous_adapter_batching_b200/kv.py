@@ -66,7 +66,8 @@ class KVCache:
     One block of `block_tokens` tokens of one layer lives in a page; a model keeps one KVCache per layer (on one pool or
     several).  A request is a row of the block table: begin() runs lora_kv_layout over the rows' lengths, handing
     out reserved pages; append() and attend() (or prompt_attend()) are the layer's calls; free() gives the pages of
-    finished rows back to the pool.
+    finished rows back to the pool.  past_len says where the new tokens go: a row whose past has become shorter (drafts
+    that were rejected, a step repeated after an error) fills the blocks it holds again before it takes any.
 
     The calls of a step may be captured in a graph and replayed: every tensor keeps its place, reserve() and free()
     between replays included.  Steps of one KVCache follow one another on one stream (they share its workspace).
@@ -87,9 +88,10 @@ class KVCache:
         self.block_table = i32(max_requests, -(-max_len // block_tokens)).fill_(-1)
         self.cu_new, self.kv_len = i32(max_requests + 1), i32(max_requests)
         self.positions, self.slots, self.ids = i32(max_tokens), i32(max_tokens), i32(max_tokens)
-        # pages in reserve: free_list[head:], so that its end, which lora_kv_layout is told, never moves
+        # pages in reserve: free_list[head:], so that its end, which lora_kv_layout is told, never moves; blocks each row holds
         self.free_list = i32(n)
-        self.head, self._next_head = i32(1).fill_(n), i32(1).fill_(n)
+        self._state, self._next = i32(1 + max_requests), i32(1 + max_requests)
+        self.head, self._next_head, self.held = self._state[:1].fill_(n), self._next[:1].fill_(n), self._state[1:]
         self.rows = 0
         self.err = i32(1)
         self.ws = torch.empty(B.lora_kv_attend_workspace_size(q_heads, kv_heads, head_dim, max_q_len), dtype=torch.uint8,
@@ -111,11 +113,11 @@ class KVCache:
         R = past_len.numel()
         B.lora_kv_layout(past_len, new_len, req_ids, self.block_tokens, self.block_table[:R], self.free_list, self.head,
                          self.cu_new[:R + 1], self.kv_len[:R], self.positions, self.slots, self.ids, self._next_head,
-                         err=self.err, stream=stream)
+                         err=self.err, stream=stream, held=self.held[:R], held_out=self._next[1:1 + R])
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=self.device)
         with torch.cuda.stream(stream):       # None: the current one
-            self.head.copy_(self._next_head)
+            self._state[:1 + R].copy_(self._next[:1 + R])
         self.rows = R
 
     def append(self, q, k, v, inv_freq, q_out, k_out=None, v_out=None, interleaved=False, mscale=1.0, stream=None) -> None:
@@ -143,4 +145,5 @@ class KVCache:
         held = self.block_table[done.to(self.device)].flatten().cpu()
         B.lora_pool_free_page_list(self.pool, held[held >= 0])
         self.block_table[done.to(self.device)] = -1
+        self.held[done.to(self.device)] = 0
         torch.cuda.synchronize(self.device)

@@ -457,7 +457,8 @@ size_t lora_kv_block_bytes(int kv_heads, int head_dim, int block_tokens);
  * of which the first ceil(past_len / block_tokens) are filled on entry.  In
  * request order, every request takes the pages its new tokens need from
  * free_pages[free_head ..] and has their ids written to its row of block_table
- * (other entries stay).  free_pages [num_free] and free_head [1] are device
+ * (other entries stay; an entry that is written over is the caller's to know of,
+ * see lora_kv_layout_held).  free_pages [num_free] and free_head [1] are device
  * arrays; free_head NULL means 0; free_pages NULL means that block_table
  * already names every block (the slots of cached tokens can be listed so).
  * Outputs (device):
@@ -482,6 +483,20 @@ int lora_kv_layout(const int32_t *past_len, const int32_t *new_len, const int32_
                    int block_tokens, int32_t *block_table, int max_blocks, const int32_t *free_pages, int num_free,
                    const int32_t *free_head, int32_t *cu_new, int32_t *kv_len, int32_t *positions, int32_t *slots,
                    int32_t *ids, int32_t *free_head_out, int32_t *err_dev, lora_stream_t stream);
+
+/* lora_kv_layout for rows that may hold more blocks than their past fills: held
+ * [R] (device) says how many blocks of request r's row, from the first, are its
+ * own.  Blocks ceil(past / block_tokens) .. held[r] keep their pages and are
+ * filled before any is taken from the list, so that a request whose past has
+ * become shorter (rejected drafts, a step repeated after an error) loses none.
+ * held[r] below the blocks of past counts as those.  held_out [R]: the same
+ * after the call, for the next one (a failed request's as it was); it does not
+ * overlap held.  held[r] outside 0 .. max_blocks: LORA_DEV_ERR_BAD_LENGTH. */
+int lora_kv_layout_held(const int32_t *past_len, const int32_t *new_len, const int32_t *req_ids, int R, int T,
+                        int block_tokens, int32_t *block_table, int max_blocks, const int32_t *free_pages, int num_free,
+                        const int32_t *free_head, int32_t *cu_new, int32_t *kv_len, int32_t *positions, int32_t *slots,
+                        int32_t *ids, int32_t *free_head_out, const int32_t *held, int32_t *held_out, int32_t *err_dev,
+                        lora_stream_t stream);
 
 /* Rotary positions.  For each row t with positions[t] >= 0 (others are left
  * alone, input and output) and each pair i < rot_dim / 2 of every head:

@@ -1,0 +1,146 @@
+"""GPU: steps of a KVCache that do not simply go on: rejected drafts, steps that
+are repeated, steps that mix prompts and decoding; no page is lost or used twice."""
+import numpy as np
+import pytest
+import torch
+
+from tests import _kv as K
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def H():
+    import heterogeneous_adapter_batching_b200 as H
+    H.load_library()
+    return H
+
+
+def i32(x):
+    return torch.as_tensor(np.ascontiguousarray(x), dtype=torch.int32).cuda()
+
+
+def make(H, n_pages=40, block=16, max_requests=3, max_len=160, max_tokens=64, hq=4, hk=2, dim=64, **kw):
+    buf = torch.empty((n_pages * 16, 256), dtype=BF, device="cuda")
+    pool = H.lora_pool_create(buf, 256)
+    return H.KVCache(pool, hq, hk, dim, block, max_requests=max_requests, max_len=max_len, max_tokens=max_tokens, **kw)
+
+
+def accounted(H, cache, reserved):
+    """Every page that was reserved is in a row of the table or in the reserve, once."""
+    torch.cuda.synchronize()
+    held = cache.block_table[cache.block_table >= 0].tolist()
+    spare = cache.free_list[int(cache.head.item()):].tolist()
+    assert len(set(held + spare)) == len(held) + len(spare) == reserved == H.lora_pool_usage(cache.pool)[1]
+    return len(held)
+
+
+def test_rejected_drafts_lose_no_page(H):
+    """A past that becomes shorter across a block's border, again and again."""
+    R, reserved = 3, 24
+    cache = make(H, max_q_len=4)
+    cache.reserve(reserved)
+    r = np.random.default_rng(1)
+    past = np.array([0, 14, 31])
+    cache.begin(i32([0, 0, 0]), i32(past))
+    for step in range(60):
+        new = r.integers(1, 5, R)
+        first = cache.block_table.cpu().numpy().copy()
+        cache.begin(i32(past), i32(new))
+        accounted(H, cache, reserved)
+        table = cache.block_table.cpu().numpy()
+        assert (table[first >= 0] == first[first >= 0]).all()          # a row's blocks stay where they are
+        at = np.concatenate([[0], np.cumsum(new)])
+        slots, pos = cache.slots.cpu().numpy(), cache.positions.cpu().numpy()
+        for q in range(R):
+            want = past[q] + np.arange(new[q])
+            assert (pos[at[q]:at[q + 1]] == want).all()
+            assert (slots[at[q]:at[q + 1]] == table[q, want // 16] * 16 + want % 16).all()
+        assert cache.kv_len.tolist() == (past + new).tolist() and int(cache.err.item()) == 0
+        past = past + r.integers(0, new + 1)                           # how many of them were accepted
+        past = np.where(past > 100, past - 40, past)                   # and a request that goes back a long way
+    cache.free([0, 1, 2])
+    spare = cache.free_list[int(cache.head.item()):].numel()
+    assert H.lora_pool_usage(cache.pool)[1] == spare and (cache.held == 0).all()
+
+
+def test_a_step_repeated_after_an_empty_reserve(H):
+    """The request that got its pages keeps them when the step is repeated for the one that got none."""
+    cache = make(H, max_requests=2)
+    cache.reserve(3)
+    past, new = i32([0, 0]), i32([20, 30])
+    cache.begin(past, new)
+    assert accounted(H, cache, 3) == 2 and int(cache.err.item()) == H.DEV_ERR_NO_PAGES and cache.kv_len.tolist() == [20, 0]
+    held = cache.block_table[0].tolist()
+    cache.reserve(5)
+    cache.err.zero_()
+    cache.begin(past, new)
+    assert accounted(H, cache, 8) == 4 and int(cache.err.item()) == 0 and cache.kv_len.tolist() == [20, 30]
+    assert cache.block_table[0].tolist() == held
+
+
+def test_a_captured_step_with_drafts(H):
+    cache = make(H, max_q_len=4)
+    cache.reserve(6)
+    past, new = i32([10, 13, 15]), i32([4, 4, 4])
+    cache.begin(i32([0, 0, 0]), past.clone())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.begin(past, new)
+    for p in ([10, 13, 15], [11, 14, 16], [12, 15, 15], [12, 12, 17]):
+        past.copy_(i32(p))
+        g.replay()
+        accounted(H, cache, 6)
+        assert cache.kv_len.tolist() == [x + 4 for x in p] and int(cache.err.item()) == 0
+    assert accounted(H, cache, 6) == 5 and cache.held.tolist() == [1, 2, 2]
+
+
+def layout_held(past, new, T, block, table, free, head, held):
+    """The rule, request by request: a request takes pages for the blocks beyond those it holds."""
+    table, at, dry, taken, out = table.copy(), head, False, 0, []
+    pos, slots, kv_len, err = [], [], [], 0
+    for r in range(len(past)):
+        p, n = int(past[r]), int(new[r])
+        first, after = max(-(-p // block), int(held[r])), -(-(p + n) // block)
+        bad = not 0 <= held[r] <= table.shape[1] or p + n > table.shape[1] * block
+        need = 0 if bad else max(0, after - first)
+        dry = dry or (need > 0 and at + need > len(free))
+        failed = bad or (need > 0 and dry)
+        err |= 32 if bad else 16 if failed else 0
+        if not failed:
+            table[r, first:first + need] = free[at:at + need]
+            taken = at + need - head if need else taken
+        at += need
+        out.append(int(held[r]) if failed else max(first, after))
+        kv_len.append(0 if failed else p + n)
+        pos += [-1 if failed else p + i for i in range(n)]
+        slots += [-1 if failed else int(table[r, (p + i) // block]) * block + (p + i) % block for i in range(n)]
+    pad = [-1] * (T - len(pos))
+    return table, kv_len, pos + pad, slots + pad, out, head + taken, err
+
+
+@pytest.mark.parametrize("R,block,width", [(1, 16, 4), (40, 16, 9), (300, 32, 6), (1024, 16, 5)])
+def test_layout_of_rows_that_hold_more(H, R, block, width):
+    r = np.random.default_rng(R)
+    held = r.integers(0, width + 1, R)
+    past = np.minimum(r.integers(0, width * block + 1, R), held * block)
+    past[r.random(R) < 0.1] = 0
+    new = np.minimum(r.integers(0, 2 * block, R), width * block - past)
+    ids = r.permutation(R * width + 7)
+    table = np.full((R, width), -1)
+    own = np.arange(width) < held[:, None]
+    table[own] = ids[:own.sum()]
+    free = ids[own.sum():][:R // 2 + 3]
+    if R > 10:
+        held[3], held[7] = -1, width + 1
+    T = int(new.sum()) + 5
+    want = layout_held(past, new, T, block, table, free, 1, held)
+    cu, kv, pos, slots, head, out, err, dt = (i32(np.full(n, -7)) for n in (R + 1, R, T, T, 1, R, 1, (R, width)))
+    err.zero_()
+    dt.copy_(i32(table))
+    H.lora_kv_layout(i32(past), i32(new), None, block, dt, i32(free), i32([1]), cu, kv, pos, slots, None, head, err=err, held=i32(held),
+                     held_out=out)
+    got = (dt.cpu().numpy(), kv.tolist(), pos.tolist(), slots.tolist(), out.tolist(), int(head.item()), int(err.item()))
+    assert np.array_equal(got[0], want[0]) and got[1:] == want[1:]

@@ -249,3 +249,16 @@ def test_rope_frequencies_refusals(rot_dim, scaling):
     from heterogeneous_adapter_batching_b200 import rope_frequencies as rf
     with pytest.raises(ValueError):
         rf(rot_dim, scaling=scaling)
+
+
+def test_layout_of_held_blocks_refusals(H):
+    lib = H.load_library()
+
+    def call(held=p(4096), held_out=p(8192), past=p(), kv=p(12288)):
+        return lib.lora_kv_layout_held(past, p(256), None, 4, 0, 16, p(512), 4, p(1024), 10, p(2048), p(2304), kv, None, None, None,
+                                       p(3072), held, held_out, None, None)
+
+    assert call(held=None) == -1 and call(held_out=None) == -1 and call(past=None) == -1
+    assert call(held_out=p(4096)) == -1 and call(held_out=p(4096 + 12)) == -1      # not in place
+    assert call(held=p(12288)) == -1 and call(held_out=p(12288)) == -1             # nor over another array
+    assert lib.lora_last_launch_count() == 0
