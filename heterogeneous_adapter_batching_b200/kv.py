@@ -71,7 +71,9 @@ class KVCache:
 
     The calls of a step may be captured in a graph and replayed: every tensor keeps its place, reserve() and free()
     between replays included.  Steps of one KVCache follow one another on one stream (they share its workspace).
-    Requests that bring more than max_q_len tokens in a step go through prompt_attend()."""
+    Requests that bring more than max_q_len tokens in a step go through prompt_attend(); a step that mixes both kinds
+    lists one kind behind the other and names the requests of each call (first, last).  prompt_attend() is for prompts
+    from their first token on; a chunk over a cached past reads it back with lora_kv_gather for lora_prompt_attend."""
 
     def __init__(self, pool: B.Pool, q_heads: int, kv_heads: int, head_dim: int, block_tokens: int, max_requests: int,
                  max_len: int, max_tokens: int, max_q_len: int = 1, dtype=torch.bfloat16):
@@ -125,15 +127,32 @@ class KVCache:
         B.lora_kv_append(q, k, v, self.positions[:T], inv_freq, self.slots[:T], self.pages, self.block_tokens, q_out, k_out,
                          v_out, interleaved=interleaved, mscale=mscale, dtype=self.dtype, err=self.err, stream=stream)
 
-    def attend(self, q, out, scale: Optional[float] = None, lse=None, stream=None) -> None:
-        R = self.rows
-        B.lora_kv_attend(q, self.pages, self.block_tokens, self.kv_heads, self.block_table[:R], self.cu_new[:R + 1],
-                         self.kv_len[:R], self.max_q_len, self.head_dim ** -0.5 if scale is None else scale, out, self.ws,
+    def _span(self, first: int, last: Optional[int]):
+        """Requests first .. last - 1 of the step as a slice."""
+        last = self.rows if last is None else last
+        if not 0 <= first <= last <= self.rows:
+            raise ValueError(f"requests {first} .. {last} of a step of {self.rows}")
+        return slice(first, last)
+
+    def attend(self, q, out, scale: Optional[float] = None, lse=None, stream=None, first: int = 0,
+               last: Optional[int] = None) -> None:
+        """Attention of the new tokens of requests first .. last - 1 (all of the step) over the cache.  q, out and lse hold
+        the rows of the whole step; those of other requests are left alone."""
+        r = self._span(first, last)
+        if r.start == r.stop:
+            return
+        B.lora_kv_attend(q, self.pages, self.block_tokens, self.kv_heads, self.block_table[r], self.cu_new[r.start:r.stop + 1],
+                         self.kv_len[r], self.max_q_len, self.head_dim ** -0.5 if scale is None else scale, out, self.ws,
                          lse=lse, err=self.err, stream=stream)
 
-    def prompt_attend(self, q, k, v, out, scale: Optional[float] = None, lse=None, stream=None) -> None:
-        """Attention among the step's own rows: requests whose past is empty."""
-        cu = self.cu_new[:self.rows + 1]
+    def prompt_attend(self, q, k, v, out, scale: Optional[float] = None, lse=None, stream=None, first: int = 0,
+                      last: Optional[int] = None) -> None:
+        """Attention among the step's own rows for requests first .. last - 1 (all of the step), rows as in attend();
+        requests whose past is empty."""
+        r = self._span(first, last)
+        if r.start == r.stop:
+            return
+        cu = self.cu_new[r.start:r.stop + 1]
         B.lora_prompt_attend(q, k, v, cu, cu, self.head_dim ** -0.5 if scale is None else scale, out, lse=lse, err=self.err,
                              stream=stream)
 

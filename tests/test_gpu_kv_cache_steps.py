@@ -144,3 +144,66 @@ def test_layout_of_rows_that_hold_more(H, R, block, width):
                      held_out=out)
     got = (dt.cpu().numpy(), kv.tolist(), pos.tolist(), slots.tolist(), out.tolist(), int(head.item()), int(err.item()))
     assert np.array_equal(got[0], want[0]) and got[1:] == want[1:]
+
+
+def fill(cache, T, seed, rot=None):
+    """Random rows of a step, appended without rotation; -> q, k, v as attention reads them."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    q, k, v = (torch.randn((T, n, cache.head_dim), generator=g, device="cuda").to(BF) for n in (cache.q_heads, cache.kv_heads, cache.kv_heads))
+    qo, ko, vo = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    cache.append(q, k, v, rot, qo, ko, vo)
+    return qo, ko, vo
+
+
+def want_rows(q, k, v, scale):
+    """softmax(scale q k^T) v in 64 bits for the last rows q [n, Hq, D] of k, v [m, Hk, D]."""
+    G, n, m = q.shape[1] // k.shape[1], q.shape[0], k.shape[0]
+    k, v = (x.double().repeat_interleave(G, 1) for x in (k, v))
+    s = torch.einsum("nhd,mhd->hnm", q.double(), k) * scale
+    s.masked_fill_(torch.arange(m, device="cuda") > (m - n) + torch.arange(n, device="cuda")[:, None], -torch.inf)
+    return torch.einsum("hnm,mhd->nhd", torch.softmax(s, -1), v)
+
+
+def near(got, want):
+    """Row by row: the output's rounding (2^-8 of each element) and that of the weights (2^-8 in a prompt, rows as long as
+    their values' sums; half as much on average, so that a norm stays below)."""
+    return bool(((got.double() - want).norm(dim=-1) <= 2.0 ** -7 * want.norm(dim=-1)).all())
+
+
+def test_a_step_that_mixes_decoding_and_prompts(H):
+    """Decoding requests first, prompts behind them: two calls, each for its own requests, nothing flagged."""
+    cache = make(H, n_pages=60, max_requests=4, max_tokens=200, max_q_len=2)
+    cache.reserve(40)
+    cache.begin(i32([0, 0]), i32([37, 50]))
+    _, k0, v0 = fill(cache, 87, 1)
+    past, new = np.array([37, 50, 0, 0]), np.array([1, 2, 70, 33])
+    cache.begin(i32(past), i32(new))
+    q, k, v = fill(cache, 106, 2)
+    out = torch.full_like(q, 7.0)
+    cache.attend(q, out, last=2)
+    assert (out[3:] == 7).all()
+    cache.prompt_attend(q, k, v, out, first=2)
+    again = torch.full_like(q, 7.0)
+    cache.prompt_attend(q, k, v, again, first=2)
+    torch.cuda.synchronize()
+    assert int(cache.err.item()) == 0 and (again[:3] == 7).all() and torch.equal(again[3:], out[3:])
+    at = [0, 1, 3, 73, 106]
+    for r in (2, 3):
+        s = slice(at[r], at[r + 1])
+        assert near(out[s], want_rows(q[s], k[s], v[s], 64 ** -0.5))
+    slots = i32(np.zeros(90))
+    H.lora_kv_layout(i32([0, 0]), i32([38, 52]), None, 16, cache.block_table[:2], None, None, i32([0] * 3), i32([0] * 2), i32([0] * 90), slots)
+    kc, vc = (torch.empty((90, 2, 64), dtype=torch.float32, device="cuda") for _ in range(2))
+    H.lora_kv_gather(cache.pages, 16, slots, kc, vc)
+    assert near(out[:1], want_rows(q[:1], kc[:38], vc[:38], 64 ** -0.5)) and near(out[1:3], want_rows(q[1:3], kc[38:], vc[38:], 64 ** -0.5))
+    cache.attend(q, out, first=4)                            # no such requests: nothing happens
+    cache.prompt_attend(q, k, v, out, first=2, last=2)
+    for bad in ((-1, 2), (0, 5), (3, 2)):
+        with pytest.raises(ValueError):
+            cache.attend(q, out, first=bad[0], last=bad[1])
+        with pytest.raises(ValueError):
+            cache.prompt_attend(q, k, v, out, first=bad[0], last=bad[1])
+    cache.attend(q, out, first=1, last=3)                    # a prompt longer than max_q_len is still refused there
+    torch.cuda.synchronize()
+    assert int(cache.err.item()) == H.DEV_ERR_BAD_LENGTH
