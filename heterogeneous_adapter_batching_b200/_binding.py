@@ -58,7 +58,7 @@ EXPORTS = [
     "lora_slot_cache_create", "lora_slot_cache_destroy", "lora_slot_cache_acquire", "lora_slot_cache_unpin",
     "lora_slot_cache_invalidate", "lora_slot_cache_lookup", "lora_slot_cache_stats",
     "lora_kv_block_bytes", "lora_kv_layout", "lora_kv_layout_held", "lora_rope", "lora_kv_append", "lora_kv_gather",
-    "lora_kv_attend_workspace_size", "lora_kv_attend", "lora_prompt_attend",
+    "lora_kv_attend_workspace_size", "lora_kv_attend", "lora_prompt_attend", "lora_prompt_attend_whole",
     "lora_set_option", "lora_get_option", "lora_last_cuda_error", "lora_last_launch_count",
 ]
 
@@ -141,6 +141,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "lora_kv_attend_workspace_size": (Z, [I, I, I, I]),
         "lora_kv_attend": (I, [V, I, I, I, V, V, I, V, V, I, I, F, V, V, V, Z, V, V]),
         "lora_prompt_attend": (I, [V, V, V, I, I, I, I, I, I, V, V, I, F, V, V, V, V]),
+        "lora_prompt_attend_whole": (I, [V, V, V, I, I, I, I, I, V, V, I, F, V, V, V, V]),
         "lora_set_option": (I, [I, I]),
         "lora_get_option": (I, [I]),
         "lora_last_cuda_error": (ctypes.c_char_p, []),
@@ -584,6 +585,21 @@ def lora_prompt_attend(q, k, v, cu_q, cu_k, scale: float, out, lse=None, err=Non
     _run(n, dev, stream, _r(n, q, dev, dt, shape), _r(n, k, dev, dt, kshape), _r(n, v, dev, dt, kshape), T, Tk, hq, hk, dim,
          DTYPES.get(dt, -1), _i(n, cu_q, dev, 1), _i(n, cu_k, dev, 1), R, scale, _r(n, out, dev, dt, shape),
          _lse(n, lse, q, dev), _i(n, err, dev, 1))
+
+
+def lora_prompt_attend_whole(q, k, v, cu, kv_len, scale: float, out, lse=None, err=None, stream=None) -> None:
+    """q, out [T, q_heads, head_dim], k, v [T, kv_heads, head_dim]; cu [R + 1], kv_len [R]."""
+    n = "lora_prompt_attend_whole"
+    dev, dt = _device(n, q), q.dtype
+    shape, kshape = q.shape, k.shape
+    T, hq, dim = _dims(n, shape)
+    Tk, hk, dk = _dims(n, kshape)
+    R = cu.numel() - 1
+    if Tk != T or dk != dim:
+        _refuse(n, f"rows of q and k: {tuple(shape)} against {tuple(kshape)}")
+    _run(n, dev, stream, _r(n, q, dev, dt, shape), _r(n, k, dev, dt, kshape), _r(n, v, dev, dt, kshape), T, hq, hk, dim,
+         DTYPES.get(dt, -1), _i(n, cu, dev, 1), _i(n, kv_len, dev, R), R, scale, _r(n, out, dev, dt, shape), _lse(n, lse, q, dev),
+         _i(n, err, dev, 1))
 
 
 def lora_set_option(key: int, value: int) -> None:

@@ -104,6 +104,7 @@ struct PromptArgs {
     float scale;
     float *lse;
     int32_t *err;
+    const int32_t *kv_len;   // may be null
 };
 int launch_prompt(const PromptArgs &a, cudaStream_t st);
 

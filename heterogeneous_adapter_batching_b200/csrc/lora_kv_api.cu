@@ -209,9 +209,9 @@ int lora_kv_attend(const lora_rows_t *q, int T, int q_heads, int dtype, const lo
     return launch_kv_attend(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
-int lora_prompt_attend(const lora_rows_t *q, const lora_rows_t *k, const lora_rows_t *v, int Tq, int Tk, int q_heads,
-                       int kv_heads, int head_dim, int dtype, const int32_t *cu_q, const int32_t *cu_k, int R,
-                       float scale, const lora_rows_t *out, float *lse, int32_t *err_dev, lora_stream_t stream) {
+static int prompt(const lora_rows_t *q, const lora_rows_t *k, const lora_rows_t *v, int Tq, int Tk, int q_heads, int kv_heads,
+                  int head_dim, int dtype, const int32_t *cu_q, const int32_t *cu_k, const int32_t *kv_len, int R, float scale,
+                  const lora_rows_t *out, float *lse, int32_t *err_dev, lora_stream_t stream) {
     reset_launch_count();
     if (!half_type(dtype) || Tq < 0 || Tk < 0 || R < 1 || !group_ok(q_heads, kv_heads) ||
         (head_dim != 64 && head_dim != 128) || !cu_q || !cu_k || !(scale >= 0.f && scale < INFINITY))
@@ -223,8 +223,24 @@ int lora_prompt_attend(const lora_rows_t *q, const lora_rows_t *k, const lora_ro
         return LORA_ERR_INVALID_ARG;
     if (!strides_ok(q, Tq, q_heads) || !strides_ok(k, Tk, kv_heads) || !strides_ok(v, Tk, kv_heads)) return LORA_ERR_INVALID_ARG;
     const PromptArgs a{rows(q), rows(k), rows(v), rows(out), Tq, Tk, q_heads, kv_heads, head_dim, dtype,
-                       cu_q, cu_k, R, scale, lse, err_dev};
+                       cu_q, cu_k, R, scale, lse, err_dev, kv_len};
     return launch_prompt(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int lora_prompt_attend(const lora_rows_t *q, const lora_rows_t *k, const lora_rows_t *v, int Tq, int Tk, int q_heads,
+                       int kv_heads, int head_dim, int dtype, const int32_t *cu_q, const int32_t *cu_k, int R,
+                       float scale, const lora_rows_t *out, float *lse, int32_t *err_dev, lora_stream_t stream) {
+    return prompt(q, k, v, Tq, Tk, q_heads, kv_heads, head_dim, dtype, cu_q, cu_k, nullptr, R, scale, out, lse, err_dev, stream);
+}
+
+int lora_prompt_attend_whole(const lora_rows_t *q, const lora_rows_t *k, const lora_rows_t *v, int T, int q_heads,
+                             int kv_heads, int head_dim, int dtype, const int32_t *cu, const int32_t *kv_len, int R,
+                             float scale, const lora_rows_t *out, float *lse, int32_t *err_dev, lora_stream_t stream) {
+    if (!kv_len) {
+        reset_launch_count();
+        return LORA_ERR_INVALID_ARG;
+    }
+    return prompt(q, k, v, T, T, q_heads, kv_heads, head_dim, dtype, cu, cu, kv_len, R, scale, out, lse, err_dev, stream);
 }
 
 }  // extern "C"

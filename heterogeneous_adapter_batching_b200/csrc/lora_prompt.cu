@@ -100,6 +100,7 @@ struct KArgs {
     uint32_t items;   // most items of row ranges that do not overlap
     float scale;
     int32_t *err;
+    const int32_t *kv_len;   // null, or what each request has with its past: no more than its rows, else it is refused
 };
 
 template <class Sm>
@@ -199,7 +200,8 @@ struct Req {
 };
 __device__ __forceinline__ Req request(const KArgs &a, int r) {
     const int q0 = a.cu_q[r], q1 = a.cu_q[r + 1], k0 = a.cu_k[r], k1 = a.cu_k[r + 1];
-    const bool bad = q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk;
+    const bool past = a.kv_len && a.kv_len[r] > (long long)q1 - q0;
+    const bool bad = past || q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk;
     return bad ? Req{0, -1, 0, 0} : Req{q0, q1 - q0, k0, k1 - k0};
 }
 // Key tiles that rows up to token `last` see.
@@ -652,7 +654,7 @@ int launch(const PromptArgs &a, cudaStream_t st) {
     KArgs k{};
     k.o = a.o.p; k.ots = a.o.ts; k.ohs = a.o.hs; k.lse = a.lse;
     k.cu_q = a.cu_q; k.cu_k = a.cu_k; k.Tq = a.Tq; k.Tk = a.Tk; k.R = a.R;
-    k.hq = a.hq; k.G = a.hq / a.hkv; k.scale = a.scale; k.err = a.err;
+    k.hq = a.hq; k.G = a.hq / a.hkv; k.scale = a.scale; k.err = a.err; k.kv_len = a.kv_len;
     k.pk = k.G & -k.G;
     k.groups = a.hq / k.pk;
     const int pair = 2 * kM / k.pk;                                     // tokens of a CTA

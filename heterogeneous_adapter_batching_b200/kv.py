@@ -147,14 +147,13 @@ class KVCache:
 
     def prompt_attend(self, q, k, v, out, scale: Optional[float] = None, lse=None, stream=None, first: int = 0,
                       last: Optional[int] = None) -> None:
-        """Attention among the step's own rows for requests first .. last - 1 (all of the step), rows as in attend();
-        requests whose past is empty."""
+        """Attention among the step's own rows for requests first .. last - 1 (all of the step), rows as in attend().  A
+        request whose past is not empty sets LORA_DEV_ERR_BAD_LENGTH and its rows are left alone."""
         r = self._span(first, last)
         if r.start == r.stop:
             return
-        cu = self.cu_new[r.start:r.stop + 1]
-        B.lora_prompt_attend(q, k, v, cu, cu, self.head_dim ** -0.5 if scale is None else scale, out, lse=lse, err=self.err,
-                             stream=stream)
+        B.lora_prompt_attend_whole(q, k, v, self.cu_new[r.start:r.stop + 1], self.kv_len[r],
+                                   self.head_dim ** -0.5 if scale is None else scale, out, lse=lse, err=self.err, stream=stream)
 
     def free(self, rows) -> None:
         """Return the pages of finished requests' rows to the pool and clear the rows.  Synchronises the device."""

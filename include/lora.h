@@ -593,6 +593,15 @@ int lora_prompt_attend(const lora_rows_t *q, const lora_rows_t *k, const lora_ro
                        int kv_heads, int head_dim, int dtype, const int32_t *cu_q, const int32_t *cu_k, int R,
                        float scale, const lora_rows_t *out, float *lse, int32_t *err_dev, lora_stream_t stream);
 
+/* lora_prompt_attend for prompts from their first token on: queries, keys and
+ * values are the same T rows, cu [R+1] says which are whose, and kv_len [R]
+ * (device) is what lora_kv_layout wrote.  A request with kv_len[r] above its
+ * rows has a past whose keys are not here: LORA_DEV_ERR_BAD_LENGTH, its rows
+ * are left alone. */
+int lora_prompt_attend_whole(const lora_rows_t *q, const lora_rows_t *k, const lora_rows_t *v, int T, int q_heads,
+                             int kv_heads, int head_dim, int dtype, const int32_t *cu, const int32_t *kv_len, int R,
+                             float scale, const lora_rows_t *out, float *lse, int32_t *err_dev, lora_stream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* Options and diagnostics (process-wide)                                   */
 /* ------------------------------------------------------------------------ */

@@ -207,3 +207,57 @@ def test_a_step_that_mixes_decoding_and_prompts(H):
     cache.attend(q, out, first=1, last=3)                    # a prompt longer than max_q_len is still refused there
     torch.cuda.synchronize()
     assert int(cache.err.item()) == H.DEV_ERR_BAD_LENGTH
+
+
+@pytest.mark.parametrize("R", [2, 40])
+def test_prompt_attention_refuses_requests_with_a_past(H, R):
+    """Their keys are not all among the step's rows: flagged, and their outputs are left alone; the others are as ever."""
+    cache = make(H, n_pages=200, max_requests=R, max_tokens=40 * R)
+    cache.reserve(150)
+    past, new = np.zeros(R, int), 20 + np.arange(R) % 11
+    past[1::3] = 17
+    cache.begin(i32(np.zeros(R)), i32(past))
+    fill(cache, int(past.sum()), 3)
+    cache.begin(i32(past), i32(new))
+    at = np.concatenate([[0], np.cumsum(new)])
+    q, k, v = fill(cache, int(at[-1]), 4)
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    cache.prompt_attend(q, k, v, out, lse=lse)
+    torch.cuda.synchronize()
+    assert int(cache.err.item()) == H.DEV_ERR_BAD_LENGTH
+    for r in range(R):
+        s = slice(at[r], at[r + 1])
+        if past[r]:
+            assert (out[s] == 7).all() and (lse[s] == 7).all()
+        else:
+            assert near(out[s], want_rows(q[s], k[s], v[s], 64 ** -0.5))
+    cache.err.zero_()
+    out.fill_(7.0)
+    cache.prompt_attend(q, k, v, out, first=0, last=1, stream=torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert int(cache.err.item()) == 0 and (out[at[1]:] == 7).all()
+    assert near(out[:at[1]], want_rows(q[:at[1]], k[:at[1]], v[:at[1]], 64 ** -0.5))
+
+
+def test_prompt_attention_in_a_graph_over_changing_lengths(H):
+    cache = make(H, max_tokens=64)
+    cache.reserve(20)
+    past, new = i32([0, 0]), i32([20, 30])
+    cache.begin(past, new)
+    q, k, v = fill(cache, 50, 5)
+    out = torch.full_like(q, 7.0)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.begin(past, new)
+        cache.prompt_attend(q, k, v, out)
+    for a, b, p in ((20, 30, 0), (1, 49, 0), (3, 4, 0), (20, 30, 5)):
+        new.copy_(i32([a, b]))
+        past.copy_(i32([0, p]))
+        out.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(cache.err.item()) == (H.DEV_ERR_BAD_LENGTH if p else 0) and (out[a + b:] == 7).all()
+        assert near(out[:a], want_rows(q[:a], k[:a], v[:a], 64 ** -0.5))
+        rest = out[a:a + b]
+        assert (rest == 7).all() if p else near(rest, want_rows(q[a:a + b], k[a:a + b], v[a:a + b], 64 ** -0.5))

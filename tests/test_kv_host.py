@@ -262,3 +262,16 @@ def test_layout_of_held_blocks_refusals(H):
     assert call(held_out=p(4096)) == -1 and call(held_out=p(4096 + 12)) == -1      # not in place
     assert call(held=p(12288)) == -1 and call(held_out=p(12288)) == -1             # nor over another array
     assert lib.lora_last_launch_count() == 0
+
+
+def test_whole_prompt_refusals(H):
+    lib = H.load_library()
+
+    def call(q=None, T=4, hq=32, hk=8, dim=128, dtype=0, cu=p(), lens=p(), R=1, scale=1.0):
+        return lib.lora_prompt_attend_whole(rows(H) if q is None else q, rows(H), rows(H), T, hq, hk, dim, dtype, cu, lens, R, scale,
+                                            rows(H), None, None, None)
+
+    assert call(T=0) == 0
+    assert call(lens=None) == -1 and call(cu=None) == -1 and call(T=-1) == -1 and call(R=0) == -1 and call(hq=31) == -1
+    assert call(q=rows(H, 8)) == -1 and call(dim=96) == -1 and call(dtype=2) == -1 and call(scale=-1.0) == -1 and call(R=4097) == -8
+    assert lib.lora_last_launch_count() == 0
