@@ -33,19 +33,17 @@ struct Need {
 };
 
 // Blocks of a request that are there before the call; the next one takes the first of its pages.
-__device__ __forceinline__ int blocks_before(const LayoutArgs &a, int r, int past) {
-    const int n = (past + a.block - 1) / a.block;
-    return a.held ? max(n, a.held[r]) : n;
+__device__ __forceinline__ int blocks_before(const LayoutArgs &a, int past, int held) {
+    return max((past + a.block - 1) / a.block, held);
 }
 
-__device__ __forceinline__ Need need_of(const LayoutArgs &a, int r, int past, int fresh) {
+__device__ __forceinline__ Need need_of(const LayoutArgs &a, int past, int fresh, int held) {
     Need n;
     n.rows = fresh < 0 ? 0 : fresh;
-    n.bad = past < 0 || fresh < 0 || (long long)past + fresh > (long long)a.max_blocks * a.block ||
-            (a.held && (a.held[r] < 0 || a.held[r] > a.max_blocks));
+    n.bad = past < 0 || fresh < 0 || (long long)past + fresh > (long long)a.max_blocks * a.block || held < 0 || held > a.max_blocks;
     n.pages = n.after = 0;
     if (n.bad) return n;
-    const int before = blocks_before(a, r, past);
+    const int before = blocks_before(a, past, held);
     n.after = max(before, (past + fresh + a.block - 1) / a.block);
     if (a.free_pages) n.pages = n.after - before;
     return n;
@@ -62,7 +60,9 @@ __device__ __forceinline__ int owner(const int *ends, int R, int x) {
     return lo;
 }
 
+template <bool HELD>
 __global__ void __launch_bounds__(kThreads) kv_layout_kernel(LayoutArgs a) {
+    const auto held_of = [&](int r) { return HELD ? a.held[r] : 0; };
     extern __shared__ int sm[];
     int *row_end = sm, *page_end = sm + a.R;                                   // running sums
     unsigned char *failed = reinterpret_cast<unsigned char *>(sm + 2 * a.R);   // per request
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) kv_layout_kernel(LayoutArgs a) {
 
     Sums mine{0, 0};
     for (int r = r0; r < r1; ++r) {
-        const Need n = need_of(a, r, a.past[r], a.fresh_len[r]);
+        const Need n = need_of(a, a.past[r], a.fresh_len[r], held_of(r));
         mine.rows += n.rows;
         mine.pages += n.pages;
     }
@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(kThreads) kv_layout_kernel(LayoutArgs a) {
     const int avail = head < 0 || head > a.num_free ? 0 : a.num_free - head;
     int flags = head < 0 || head > a.num_free ? LORA_DEV_ERR_NO_PAGES : 0;
     for (int r = r0; r < r1; ++r) {
-        const int past = a.past[r], fresh = a.fresh_len[r];
-        const Need n = need_of(a, r, past, fresh);
+        const int past = a.past[r], fresh = a.fresh_len[r], held = held_of(r);
+        const Need n = need_of(a, past, fresh, held);
         run.rows += n.rows;
         run.pages += n.pages;
         bool f = n.bad || (n.rows > 0 && run.rows > a.T);
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) kv_layout_kernel(LayoutArgs a) {
             if (r == 0) a.cu[0] = 0;
             a.cu[r + 1] = row_end[r];
             a.kv_len[r] = f ? 0 : past + fresh;
-            if (a.held_out) a.held_out[r] = f ? a.held[r] : n.after;
+            if (HELD) a.held_out[r] = f ? held : n.after;
         }
     }
     __syncthreads();
@@ -130,14 +130,14 @@ __global__ void __launch_bounds__(kThreads) kv_layout_kernel(LayoutArgs a) {
         const int r = owner(page_end, a.R, j);
         if (failed[r]) continue;
         const int start = r ? page_end[r - 1] : 0;
-        a.table[(size_t)r * a.max_blocks + blocks_before(a, r, a.past[r]) + j - start] = a.free_pages[head + j];
+        a.table[(size_t)r * a.max_blocks + blocks_before(a, a.past[r], held_of(r)) + j - start] = a.free_pages[head + j];
     }
     const int used = row_end[a.R - 1];
     for (int t = me; t < a.T; t += all) {
         int pos = -1, slot = -1, id = -1;
         const int r = t < used ? owner(row_end, a.R, t) : 0;
         if (t < used && !failed[r]) {
-            const int past = a.past[r], before = blocks_before(a, r, past);
+            const int past = a.past[r], before = blocks_before(a, past, held_of(r));
             pos = past + t - (r ? row_end[r - 1] : 0);
             const int blk = pos / a.block;
             const int page = a.free_pages && blk >= before ? a.free_pages[head + (r ? page_end[r - 1] : 0) + blk - before]
@@ -163,7 +163,8 @@ int launch_kv_layout(const LayoutArgs &a, cudaStream_t st) {
     int grid = (work + kThreads - 1) / kThreads;
     if (grid > 592) grid = 592;
     const size_t smem = (size_t)a.R * 9;
-    kv_layout_kernel<<<grid, kThreads, smem, st>>>(a);
+    if (a.held) kv_layout_kernel<true><<<grid, kThreads, smem, st>>>(a);
+    else kv_layout_kernel<false><<<grid, kThreads, smem, st>>>(a);
     count_launch();
     return cuda_check(cudaGetLastError());
 }

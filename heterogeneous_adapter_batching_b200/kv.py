@@ -90,11 +90,11 @@ class KVCache:
         self.block_table = i32(max_requests, -(-max_len // block_tokens)).fill_(-1)
         self.cu_new, self.kv_len = i32(max_requests + 1), i32(max_requests)
         self.positions, self.slots, self.ids = i32(max_tokens), i32(max_tokens), i32(max_tokens)
-        # pages in reserve: free_list[head:], so that its end, which lora_kv_layout is told, never moves; blocks each row holds
+        # pages in reserve: free_list[head:], so that its end, which lora_kv_layout is told, never moves; held: blocks of each row
         self.free_list = i32(n)
         self._state, self._next = i32(1 + max_requests), i32(1 + max_requests)
         self.head, self._next_head, self.held = self._state[:1].fill_(n), self._next[:1].fill_(n), self._state[1:]
-        self.rows = 0
+        self.rows, self._views = 0, None
         self.err = i32(1)
         self.ws = torch.empty(B.lora_kv_attend_workspace_size(q_heads, kv_heads, head_dim, max_q_len), dtype=torch.uint8,
                               device=dev)
@@ -113,13 +113,17 @@ class KVCache:
         """lora_kv_layout over rows 0 .. R-1 of the block table (past_len, new_len, req_ids [R] int32 on the device;
         past_len is not this object's kv_len, which the call writes)."""
         R = past_len.numel()
-        B.lora_kv_layout(past_len, new_len, req_ids, self.block_tokens, self.block_table[:R], self.free_list, self.head,
-                         self.cu_new[:R + 1], self.kv_len[:R], self.positions, self.slots, self.ids, self._next_head,
-                         err=self.err, stream=stream, held=self.held[:R], held_out=self._next[1:1 + R])
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=self.device)
-        with torch.cuda.stream(stream):       # None: the current one
-            self._state[:1 + R].copy_(self._next[:1 + R])
+        table, cu_new, kv_len, held, held_out, state, after = self._slices(R)
+        B.lora_kv_layout(past_len, new_len, req_ids, self.block_tokens, table, self.free_list, self.head, cu_new, kv_len,
+                         self.positions, self.slots, self.ids, self._next_head, err=self.err, stream=stream, held=held,
+                         held_out=held_out)
+        if stream is None:
+            state.copy_(after)
+        else:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=self.device)
+            with torch.cuda.stream(stream):
+                state.copy_(after)
         self.rows = R
 
     def append(self, q, k, v, inv_freq, q_out, k_out=None, v_out=None, interleaved=False, mscale=1.0, stream=None) -> None:
@@ -127,33 +131,40 @@ class KVCache:
         B.lora_kv_append(q, k, v, self.positions[:T], inv_freq, self.slots[:T], self.pages, self.block_tokens, q_out, k_out,
                          v_out, interleaved=interleaved, mscale=mscale, dtype=self.dtype, err=self.err, stream=stream)
 
-    def _span(self, first: int, last: Optional[int]):
-        """Requests first .. last - 1 of the step as a slice."""
+    def _slices(self, R: int):
+        """The tensors of a step of R requests; made once, as steps mostly have as many as the last."""
+        own = (R, self.block_table, self.cu_new, self.kv_len)
+        if self._views is None or any(a is not b for a, b in zip(self._views[0][1:], own[1:])) or self._views[0][0] != R:
+            self._views = (own, (self.block_table[:R], self.cu_new[:R + 1], self.kv_len[:R], self.held[:R], self._next[1:1 + R],
+                                 self._state[:1 + R], self._next[:1 + R]))
+        return self._views[1]
+
+    def _requests(self, first: int, last: Optional[int]):
+        """(block table, row starts, lengths) of requests first .. last - 1 of the step; None if there are none."""
+        if first == 0 and last is None:
+            return self._slices(self.rows)[:3]
         last = self.rows if last is None else last
         if not 0 <= first <= last <= self.rows:
             raise ValueError(f"requests {first} .. {last} of a step of {self.rows}")
-        return slice(first, last)
+        return (self.block_table[first:last], self.cu_new[first:last + 1], self.kv_len[first:last]) if first < last else None
 
     def attend(self, q, out, scale: Optional[float] = None, lse=None, stream=None, first: int = 0,
                last: Optional[int] = None) -> None:
         """Attention of the new tokens of requests first .. last - 1 (all of the step) over the cache.  q, out and lse hold
         the rows of the whole step; those of other requests are left alone."""
-        r = self._span(first, last)
-        if r.start == r.stop:
-            return
-        B.lora_kv_attend(q, self.pages, self.block_tokens, self.kv_heads, self.block_table[r], self.cu_new[r.start:r.stop + 1],
-                         self.kv_len[r], self.max_q_len, self.head_dim ** -0.5 if scale is None else scale, out, self.ws,
-                         lse=lse, err=self.err, stream=stream)
+        r = self._requests(first, last)
+        if r:
+            B.lora_kv_attend(q, self.pages, self.block_tokens, self.kv_heads, *r, self.max_q_len,
+                             self.head_dim ** -0.5 if scale is None else scale, out, self.ws, lse=lse, err=self.err, stream=stream)
 
     def prompt_attend(self, q, k, v, out, scale: Optional[float] = None, lse=None, stream=None, first: int = 0,
                       last: Optional[int] = None) -> None:
         """Attention among the step's own rows for requests first .. last - 1 (all of the step), rows as in attend().  A
         request whose past is not empty sets LORA_DEV_ERR_BAD_LENGTH and its rows are left alone."""
-        r = self._span(first, last)
-        if r.start == r.stop:
-            return
-        B.lora_prompt_attend_whole(q, k, v, self.cu_new[r.start:r.stop + 1], self.kv_len[r],
-                                   self.head_dim ** -0.5 if scale is None else scale, out, lse=lse, err=self.err, stream=stream)
+        r = self._requests(first, last)
+        if r:
+            B.lora_prompt_attend_whole(q, k, v, r[1], r[2], self.head_dim ** -0.5 if scale is None else scale, out, lse=lse,
+                                       err=self.err, stream=stream)
 
     def free(self, rows) -> None:
         """Return the pages of finished requests' rows to the pool and clear the rows.  Synchronises the device."""

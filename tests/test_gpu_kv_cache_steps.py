@@ -261,3 +261,25 @@ def test_prompt_attention_in_a_graph_over_changing_lengths(H):
         assert near(out[:a], want_rows(q[:a], k[:a], v[:a], 64 ** -0.5))
         rest = out[a:a + b]
         assert (rest == 7).all() if p else near(rest, want_rows(q[a:a + b], k[a:a + b], v[a:a + b], 64 ** -0.5))
+
+
+def test_steps_of_different_sizes_and_tensors_put_in_place_of_others(H):
+    """The slices that a step reuses follow the number of requests, and the object's tensors."""
+    cache = make(H, max_tokens=8)
+    cache.reserve(20)
+    for R in (3, 1, 3, 2):
+        cache.begin(i32([0] * R), i32([2] * R))
+        assert cache.cu_new[:R + 1].tolist() == [2 * i for i in range(R + 1)] and cache.kv_len[:R].tolist() == [2] * R
+        q, k, v = fill(cache, 2 * R, R)
+        out = torch.empty_like(q)
+        cache.prompt_attend(q, k, v, out)
+        for r in range(R):
+            s = slice(2 * r, 2 * r + 2)
+            assert near(out[s], want_rows(q[s], k[s], v[s], 64 ** -0.5))
+    other = torch.full_like(cache.block_table, -1)
+    other[0, 0] = 39
+    cache.block_table = other
+    cache.held.zero_()
+    cache.begin(i32([1, 0]), i32([1, 1]))
+    torch.cuda.synchronize()
+    assert cache.slots[:2].tolist() == [39 * 16 + 1, int(other[1, 0]) * 16] and int(cache.err.item()) == 0
