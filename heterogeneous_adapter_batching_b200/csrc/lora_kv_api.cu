@@ -13,9 +13,9 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 int elem_size(int dtype) { return dtype == LORA_FP32 ? 4 : 2; }
 
-// Row tensor checks; heads = 0 makes any (also a missing) tensor fine.
-bool rows_ok(const lora_rows_t *r, int heads, int dtype) {
-    if (heads == 0) return true;
+// Row tensor checks; without tokens or heads any tensor is fine, also one that is missing or has no address.
+bool rows_ok(const lora_rows_t *r, int T, int heads, int dtype) {
+    if (T == 0 || heads == 0) return true;
     if (!r || !r->data || !aligned16(r->data) || r->token_stride < 0 || r->head_stride < 0) return false;
     const int64_t e = 16 / elem_size(dtype);
     return r->token_stride % e == 0 && r->head_stride % e == 0;
@@ -23,7 +23,7 @@ bool rows_ok(const lora_rows_t *r, int heads, int dtype) {
 
 // Output rows: also apart from one another.
 bool out_ok(const lora_rows_t *r, int T, int heads, int dim, int dtype) {
-    return rows_ok(r, heads, dtype) && (heads == 0 || ((T < 2 || r->token_stride >= dim) && (heads < 2 || r->head_stride >= dim)));
+    return rows_ok(r, T, heads, dtype) && (T == 0 || heads == 0 || ((T < 2 || r->token_stride >= dim) && (heads < 2 || r->head_stride >= dim)));
 }
 
 // n int32 of an array; none where there is no array.
@@ -126,7 +126,7 @@ int lora_rope(const lora_rows_t *q, int q_heads, const lora_rows_t *k, int k_hea
     if (!rope_ok(src_dtype, dst_dtype, T, head_dim, positions, inv_freq, rot_dim) || q_heads < 0 || k_heads < 0 ||
         q_heads > 4096 || k_heads > 4096)
         return LORA_ERR_INVALID_ARG;
-    if (!rows_ok(q, q_heads, src_dtype) || !rows_ok(k, k_heads, src_dtype) || !out_ok(q_out, T, q_heads, head_dim, dst_dtype) ||
+    if (!rows_ok(q, T, q_heads, src_dtype) || !rows_ok(k, T, k_heads, src_dtype) || !out_ok(q_out, T, q_heads, head_dim, dst_dtype) ||
         !out_ok(k_out, T, k_heads, head_dim, dst_dtype))
         return LORA_ERR_INVALID_ARG;
     if (T == 0 || q_heads + k_heads == 0) return LORA_OK;
@@ -149,7 +149,7 @@ int lora_kv_append(const lora_rows_t *q, int q_heads, const lora_rows_t *k, cons
     if (!rope_ok(src_dtype, dst_dtype, T, kv->head_dim, positions, inv_freq, rot_dim) || q_heads < 0 || q_heads > 4096 ||
         (T > 0 && !slots))
         return LORA_ERR_INVALID_ARG;
-    if (!rows_ok(q, q_heads, src_dtype) || !rows_ok(k, h, src_dtype) || !rows_ok(v, h, src_dtype) ||
+    if (!rows_ok(q, T, q_heads, src_dtype) || !rows_ok(k, T, h, src_dtype) || !rows_ok(v, T, h, src_dtype) ||
         !out_ok(q_out, T, q_heads, kv->head_dim, dst_dtype) || !out_ok(k_out, T, k_out ? h : 0, kv->head_dim, dst_dtype) ||
         !out_ok(v_out, T, v_out ? h : 0, kv->head_dim, dst_dtype))
         return LORA_ERR_INVALID_ARG;
@@ -202,7 +202,7 @@ int lora_kv_attend(const lora_rows_t *q, int T, int q_heads, int dtype, const lo
         return LORA_ERR_WORKSPACE;
     if (T == 0) return LORA_OK;
     if ((long long)T * (q_heads / kv->kv_heads) > INT32_MAX) return LORA_ERR_TOO_LARGE;
-    if (!rows_ok(q, q_heads, dtype) || !out_ok(out, T, q_heads, kv->head_dim, dtype)) return LORA_ERR_INVALID_ARG;
+    if (!rows_ok(q, T, q_heads, dtype) || !out_ok(out, T, q_heads, kv->head_dim, dtype)) return LORA_ERR_INVALID_ARG;
     const int group = q_heads / kv->kv_heads;
     const AttendArgs a{rows(q), rows(out), T, q_heads, kv->head_dim, dtype, cache(kv), block_table, max_blocks, cu_q,
                        kv_len, R, max_q_len, scale, lse, ws, err_dev, group, 65536u / (uint32_t)group + 1};
@@ -218,8 +218,8 @@ static int prompt(const lora_rows_t *q, const lora_rows_t *k, const lora_rows_t 
         return LORA_ERR_INVALID_ARG;
     if (R > LORA_KV_MAX_REQUESTS || (long long)Tq * (q_heads / kv_heads) > INT32_MAX) return LORA_ERR_TOO_LARGE;
     if (Tq == 0) return LORA_OK;
-    if (!rows_ok(q, q_heads, dtype) || !out_ok(out, Tq, q_heads, head_dim, dtype) || !rows_ok(k, Tk ? kv_heads : 0, dtype) ||
-        !rows_ok(v, Tk ? kv_heads : 0, dtype))
+    if (!rows_ok(q, Tq, q_heads, dtype) || !out_ok(out, Tq, q_heads, head_dim, dtype) || !rows_ok(k, Tk, kv_heads, dtype) ||
+        !rows_ok(v, Tk, kv_heads, dtype))
         return LORA_ERR_INVALID_ARG;
     if (!strides_ok(q, Tq, q_heads) || !strides_ok(k, Tk, kv_heads) || !strides_ok(v, Tk, kv_heads)) return LORA_ERR_INVALID_ARG;
     const PromptArgs a{rows(q), rows(k), rows(v), rows(out), Tq, Tk, q_heads, kv_heads, head_dim, dtype,

@@ -414,6 +414,7 @@ int lora_slot_cache_stats(lora_slot_cache_t c, int64_t *hits, int64_t *misses, i
  * + h * head_stride + d].  data is 16-byte aligned and both strides are
  * multiples of 16 bytes, else LORA_ERR_INVALID_ARG: a column block of a fused
  * projection output is fine.  Strides count elements and are not negative.
+ * Without tokens (T = 0) or heads nothing is looked at, and data may be NULL.
  * The rows of an output are distinct (its strides at least head_dim where there
  * is more than one token or head, else LORA_ERR_INVALID_ARG) and overlap no
  * input, except where a call allows working in place. */

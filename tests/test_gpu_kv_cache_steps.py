@@ -283,3 +283,23 @@ def test_steps_of_different_sizes_and_tensors_put_in_place_of_others(H):
     cache.begin(i32([1, 0]), i32([1, 1]))
     torch.cuda.synchronize()
     assert cache.slots[:2].tolist() == [39 * 16 + 1, int(other[1, 0]) * 16] and int(cache.err.item()) == 0
+
+
+def test_a_step_without_tokens(H):
+    """Empty rows go through every call of a step and change nothing."""
+    cache = make(H)
+    cache.reserve(3)
+    cache.begin(i32([0, 0]), i32([5, 6]))
+    fill(cache, 11, 1)
+    torch.cuda.synchronize()
+    before = cache.pages.clone()
+    cache.begin(i32([5, 6]), i32([0, 0]))
+    f = H.rope_frequencies(64)[0].cuda()
+    q, k, v = fill(cache, 0, 2, f)
+    out, lse = torch.empty_like(q), torch.empty((0, 4), device="cuda")
+    cache.attend(q, out, lse=lse)
+    cache.prompt_attend(q, k, v, out, lse=lse)
+    H.lora_rope(q, k, cache.positions[:0], f, torch.empty_like(q), torch.empty_like(k))
+    H.lora_kv_gather(cache.pages, 16, cache.slots[:0], k, v)
+    torch.cuda.synchronize()
+    assert int(cache.err.item()) == 0 and torch.equal(cache.pages, before) and cache.kv_len[:2].tolist() == [5, 6]

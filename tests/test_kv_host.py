@@ -275,3 +275,19 @@ def test_whole_prompt_refusals(H):
     assert call(lens=None) == -1 and call(cu=None) == -1 and call(T=-1) == -1 and call(R=0) == -1 and call(hq=31) == -1
     assert call(q=rows(H, 8)) == -1 and call(dim=96) == -1 and call(dtype=2) == -1 and call(scale=-1.0) == -1 and call(R=4097) == -8
     assert lib.lora_last_launch_count() == 0
+
+
+def test_no_rows_need_no_memory(H):
+    """A step without tokens: the rows of an empty tensor have no address."""
+    lib = H.load_library()
+    none = ctypes.byref(H.LoraRows(None, 0, 0))
+    assert lib.lora_rope(none, 8, none, 2, 2, 0, 128, None, p(), 128, 0, 1.0, none, none, 0, None) == 0
+    assert lib.lora_kv_append(none, 8, none, none, 2, 0, None, p(), 128, 0, 1.0, None, cache(H), none, none, none, 0, None, None) == 0
+    assert lib.lora_kv_gather(cache(H), None, 0, none, none, 0, None, None) == 0
+    n = H.lora_kv_attend_workspace_size(32, 8, 128, 1)
+    assert lib.lora_kv_attend(none, 0, 32, 0, cache(H), p(), 4, p(), p(), 4, 1, 1.0, none, None, p(), n, None, None) == 0
+    assert lib.lora_prompt_attend(none, none, none, 0, 0, 32, 8, 128, 0, p(), p(), 1, 1.0, none, None, None, None) == 0
+    # rows that are there need theirs as ever
+    assert lib.lora_rope(none, 8, None, 0, 2, 1, 128, p(), p(), 128, 0, 1.0, rows(H), None, 0, None) == -1
+    assert lib.lora_kv_gather(cache(H), p(), 1, none, None, 0, None, None) == -1
+    assert lib.lora_last_launch_count() == 0
