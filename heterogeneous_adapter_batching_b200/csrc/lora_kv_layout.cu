@@ -125,20 +125,21 @@ __global__ void __launch_bounds__(kThreads) kv_layout_kernel(LayoutArgs a) {
         if (tid == 0 && a.head_out) *a.head_out = head + last_page;
     }
 
-    const int me = blockIdx.x * kThreads + tid, all = gridDim.x * kThreads;
-    for (int j = me; j < last_page; j += all) {
-        const int r = owner(page_end, a.R, j);
+    // 32 bits without a sign: a last step beyond 2^31 rows does not turn back
+    const unsigned me = blockIdx.x * kThreads + tid, all = gridDim.x * kThreads;
+    for (unsigned j = me; j < (unsigned)last_page; j += all) {
+        const int r = owner(page_end, a.R, (int)j);
         if (failed[r]) continue;
         const int start = r ? page_end[r - 1] : 0;
         a.table[(size_t)r * a.max_blocks + blocks_before(a, a.past[r], held_of(r)) + j - start] = a.free_pages[head + j];
     }
-    const int used = row_end[a.R - 1];
-    for (int t = me; t < a.T; t += all) {
+    const unsigned used = row_end[a.R - 1];
+    for (unsigned t = me; t < (unsigned)a.T; t += all) {
         int pos = -1, slot = -1, id = -1;
-        const int r = t < used ? owner(row_end, a.R, t) : 0;
+        const int r = t < used ? owner(row_end, a.R, (int)t) : 0;
         if (t < used && !failed[r]) {
             const int past = a.past[r], before = blocks_before(a, past, held_of(r));
-            pos = past + t - (r ? row_end[r - 1] : 0);
+            pos = past + (int)t - (r ? row_end[r - 1] : 0);
             const int blk = pos / a.block;
             const int page = a.free_pages && blk >= before ? a.free_pages[head + (r ? page_end[r - 1] : 0) + blk - before]
                                                            : a.table[(size_t)r * a.max_blocks + blk];
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) kv_layout_kernel(LayoutArgs a) {
 
 int launch_kv_layout(const LayoutArgs &a, cudaStream_t st) {
     const int work = a.T > a.R ? a.T : a.R;
-    int grid = (work + kThreads - 1) / kThreads;
+    int grid = (work - 1) / kThreads + 1;   // R is at least 1
     if (grid > 592) grid = 592;
     const size_t smem = (size_t)a.R * 9;
     if (a.held) kv_layout_kernel<true><<<grid, kThreads, smem, st>>>(a);

@@ -357,7 +357,7 @@ int rope_types(const RopeArgs &a, cudaStream_t st) {
     // wait for the angles (with the cache, 32 + 8 + 8 heads of 128: 8.5 against 10.5 us at 256 tokens, 78 against 74 us at
     // 8101; CTAs of 256 threads with four tokens take 81 us).
     const int per = a.T >= 1184 ? kMaxTok : 1;
-    const int grid = (a.T + per - 1) / per;
+    const int grid = (a.T - 1) / per + 1;   // T is at least 1
     const size_t pairs = (size_t)per * (a.rot / 2);
     if (a.slots)
         rope_kernel<S, D, true><<<grid, kThreads, pairs * (sizeof(double2) + sizeof(float2)), st>>>(a, per);
@@ -376,7 +376,7 @@ int launch_rope(const RopeArgs &a, int src, int dst, cudaStream_t st) {
 }
 
 int launch_kv_gather(const GatherKvArgs &a, int dst, cudaStream_t st) {
-    const int per = a.T >= 1184 ? kMaxTok : 1, grid = (a.T + per - 1) / per;
+    const int per = a.T >= 1184 ? kMaxTok : 1, grid = (a.T - 1) / per + 1;
     if (dst == LORA_BF16) kv_gather_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, per);
     else if (dst == LORA_FP16) kv_gather_kernel<__half><<<grid, kThreads, 0, st>>>(a, per);
     else kv_gather_kernel<float><<<grid, kThreads, 0, st>>>(a, per);

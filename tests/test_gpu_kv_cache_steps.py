@@ -303,3 +303,30 @@ def test_a_step_without_tokens(H):
     H.lora_kv_gather(cache.pages, 16, cache.slots[:0], k, v)
     torch.cuda.synchronize()
     assert int(cache.err.item()) == 0 and torch.equal(cache.pages, before) and cache.kv_len[:2].tolist() == [5, 6]
+
+
+def test_as_many_rows_as_an_int_counts(H):
+    """The last rows of 2^31 - 1: no index turns back, no grid is refused."""
+    T = 2 ** 31 - 1
+    pos, slots, err = torch.empty(T, dtype=torch.int32, device="cuda"), torch.empty(T, dtype=torch.int32, device="cuda"), i32([0])
+    table = i32([[3, -1], [5, -1]])
+    H.lora_kv_layout(i32([7, 0]), i32([12, 3]), None, 16, table, i32([8, 9]), None, i32([0] * 3), i32([0] * 2), pos, slots, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and pos[:15].tolist() == list(range(7, 19)) + [0, 1, 2]
+    assert slots[:15].tolist() == [3 * 16 + i for i in range(7, 16)] + [8 * 16 + i for i in range(3)] + [9 * 16 + i for i in range(3)]
+    for x in (pos, slots):                                   # in pieces: a comparison takes as many bytes as rows
+        assert all(bool((x[i:i + (1 << 28)] == -1).all()) for i in range(15, T, 1 << 28))
+    del slots
+    pos[T - 1] = 4
+    q = torch.randn((1, 1, 16), device="cuda").to(BF)
+    out = torch.empty((T, 1, 16), dtype=BF, device="cuda")
+    out[:3], out[T - 3:] = 7.0, 7.0
+    f = H.rope_frequencies(16)[0].cuda()
+    H.lora_rope(q.expand(T, 1, 16), None, pos, f, out)
+    one = torch.empty((1, 1, 16), dtype=BF, device="cuda")
+    H.lora_rope(q, None, i32([4]), f, one)
+    last = out[T - 3:].clone()
+    torch.cuda.synchronize()
+    assert (last[:2] == 7).all() and torch.equal(last[2], one[0])
+    del out, pos
+    torch.cuda.empty_cache()
