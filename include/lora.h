@@ -473,11 +473,16 @@ size_t lora_kv_block_bytes(int kv_heads, int head_dim, int block_tokens);
  * Rows past cu_new[R] get -1 in positions, slots and ids, which every call
  * below and lora_plan skip.  Outputs overlap neither inputs nor one another
  * (LORA_ERR_INVALID_ARG): kv_len is not past_len, free_head_out not free_head.  R in 1..LORA_KV_MAX_REQUESTS, T >= 0.
- * A request fails, alone, when a length is negative or past + new exceeds
- * max_blocks * block_tokens (or its rows exceed T): LORA_DEV_ERR_BAD_LENGTH; or
- * when the list is too short for it: LORA_DEV_ERR_NO_PAGES.  It takes no
- * pages, kv_len is 0 and its rows (min(new_len, what is left of T)) get -1
- * everywhere.  A row whose block has a negative page id gets slot -1 and
+ * A request is refused when a length is negative or past + new exceeds
+ * max_blocks * block_tokens: LORA_DEV_ERR_BAD_LENGTH; when the rows of the
+ * requests up to it exceed T: LORA_DEV_ERR_BAD_LENGTH; or when the pages that
+ * the requests up to it need exceed the list: LORA_DEV_ERR_NO_PAGES.  Rows and
+ * pages of refused requests count in these sums (pages not where a length is at
+ * fault), so that nobody overtakes a request that waits for pages: once one goes
+ * without, so does every later one that needs any, while those that need none
+ * are served.  A refused request takes no pages, kv_len is 0 and its rows
+ * (min(new_len, what is left of T)) get -1 everywhere; the others are as ever.
+ * A row whose block has a negative page id gets slot -1 and
  * LORA_DEV_ERR_BAD_PAGE. */
 #define LORA_KV_MAX_REQUESTS 4096
 int lora_kv_layout(const int32_t *past_len, const int32_t *new_len, const int32_t *req_ids, int R, int T,

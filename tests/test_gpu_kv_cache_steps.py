@@ -330,3 +330,24 @@ def test_as_many_rows_as_an_int_counts(H):
     assert (last[:2] == 7).all() and torch.equal(last[2], one[0])
     del out, pos
     torch.cuda.empty_cache()
+
+
+def test_nobody_overtakes_a_request_that_waits_for_pages(H):
+    """Pages that a refused request asked for stay with it: later requests that need any are refused, those that need none are
+    served, and what was handed out before it stands.  A request refused for its lengths holds nothing back."""
+    past, new = [0, 0, 5, 15, 0, 3], [10, 70, 3, 4, 1, 2]     # needs 1, 5, 0, 1, 1, 0 pages of a list of 4
+    table = np.full((6, 5), -1)
+    table[2, 0], table[3, 0], table[5, 0] = 40, 41, 42
+    T = 101
+
+    def run(past, new):
+        d, cu, kv, pos, slots, head, err = i32(table), i32([0] * 7), i32([0] * 6), i32([0] * T), i32([0] * T), i32([0]), i32([0])
+        H.lora_kv_layout(i32(past), i32(new), None, 16, d, i32([60, 61, 62, 63]), i32([0]), cu, kv, pos, slots, None, head, err=err)
+        return d.cpu().numpy(), kv.tolist(), slots.tolist(), int(head.item()), int(err.item())
+    d, kv, slots, head, err = run(past, new)
+    assert err == H.DEV_ERR_NO_PAGES and kv == [10, 0, 8, 0, 0, 5] and head == 1
+    assert d[0].tolist() == [60, -1, -1, -1, -1] and (d[1:] == table[1:]).all()
+    assert slots[:10] == [960 + i for i in range(10)] and slots[10:80] == [-1] * 70 and slots[80:83] == [645, 646, 647]
+    assert slots[83:88] == [-1] * 5 and slots[88:90] == [675, 676]
+    d, kv, slots, head, err = run(past, [10, 81, 3, 4, 1, 2])   # the second is too long for its row of the table
+    assert err == H.DEV_ERR_BAD_LENGTH and kv == [10, 0, 8, 19, 1, 5] and head == 3 and d[3, 1] == 61 and d[4, 0] == 62
