@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import glob
 import os
+import re
 import subprocess
 import sys
 
@@ -19,6 +20,19 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC",
     "--expt-relaxed-constexpr",
 ]
+
+# Kernels whose launches count on an exact number of registers a thread: prompt_kernel hands the registers that its block was
+# launched with from one warpgroup to the others, and a thread that asks for more than there are waits for good.
+EXACT_REGISTERS = {"lora_prompt.cu": ("prompt_kernel", 168)}
+
+
+def check_registers(log: str, kernel: str, count: int) -> int:
+    """Instances of `kernel` in the output of `ptxas -v`; RuntimeError if one has another number of registers, or there is none."""
+    found = re.findall(r"Compiling entry function '(\S*%s\S*)'.*?Used (\d+) registers" % kernel, log, re.S)
+    wrong = [(name, int(n)) for name, n in found if int(n) != count]
+    if wrong or not found:
+        raise RuntimeError(f"{kernel} needs {count} registers a thread: {wrong or 'not found in the output of ptxas -v'}")
+    return len(found)
 
 
 def sources():
@@ -44,7 +58,15 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         cmd = [NVCC, *NVCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
-        subprocess.check_call(cmd)
+        need = EXACT_REGISTERS.get(os.path.basename(src))
+        if need:
+            done = subprocess.run([*cmd, "-Xptxas", "-v"], stderr=subprocess.PIPE, text=True)
+            if verbose or done.returncode:
+                print(done.stderr, file=sys.stderr)
+            done.check_returncode()
+            check_registers(done.stderr, *need)
+        else:
+            subprocess.check_call(cmd)
         objs.append(obj)
     tmp = LIB + ".tmp"
     cmd = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs]

@@ -676,7 +676,8 @@ int launch(const PromptArgs &a, cudaStream_t st) {
     if (dev >= 64 || !(done.load() >> dev & 1)) {
         cudaFuncAttributes fa;
         if (int rc = cuda_check(cudaFuncGetAttributes(&fa, prompt_kernel<DIM, BF>))) return rc;
-        if (fa.numRegs != 168) return LORA_ERR_CUDA;   // the row owners would wait for registers that the block does not have
+        // the row owners would wait for registers that the block does not have; build.py refuses such a build
+        if (fa.numRegs != 168) return LORA_ERR_CUDA;
     }
     if (int rc = allow_smem(prompt_kernel<DIM, BF>, smem, done, dev)) return rc;
     if (int rc = cuda_check(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev))) return rc;

@@ -291,3 +291,17 @@ def test_no_rows_need_no_memory(H):
     assert lib.lora_rope(none, 8, None, 0, 2, 1, 128, p(), p(), 128, 0, 1.0, rows(H), None, 0, None) == -1
     assert lib.lora_kv_gather(cache(H), p(), 1, none, None, 0, None, None) == -1
     assert lib.lora_last_launch_count() == 0
+
+
+def test_a_build_with_other_register_counts_is_refused(H):
+    """The prompt kernel's register split holds for the count it was written for; another compiler's fails in the build."""
+    from heterogeneous_adapter_batching_b200 import build
+    line = ("ptxas info    : Compiling entry function '_ZN4lora1{0}' for 'sm_100a'\nptxas info    : Function properties for _ZN4lora1{0}\n"
+            "    8 bytes stack frame, 24 bytes spill stores, 12 bytes spill loads\nptxas info    : Used {1} registers, used 1 barriers\n")
+    other = line.format("kv_join_kernelILi64E", 32)
+    good = line.format("prompt_kernelILi128E", 168) + other + line.format("prompt_kernelILi64E", 168)
+    assert build.check_registers(good, "prompt_kernel", 168) == 2
+    for bad in (good + line.format("prompt_kernelILi64ELb1E", 160), good.replace("168", "255"), other, ""):
+        with pytest.raises(RuntimeError, match="prompt_kernel"):
+            build.check_registers(bad, "prompt_kernel", 168)
+    assert set(build.EXACT_REGISTERS) <= {p.rsplit("/", 1)[-1] for p in build.sources()}
