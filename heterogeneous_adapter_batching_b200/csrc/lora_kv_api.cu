@@ -194,7 +194,7 @@ int lora_kv_attend(const lora_rows_t *q, int T, int q_heads, int dtype, const lo
     reset_launch_count();
     if (int rc = check_cache(kv)) return rc;
     if (!half_type(dtype) || T < 0 || R < 1 || max_q_len < 1 || max_blocks < 1 || !group_ok(q_heads, kv->kv_heads) ||
-        !block_table || !cu_q || !kv_len)
+        !block_table || !cu_q || !kv_len || !std::isfinite(scale))
         return LORA_ERR_INVALID_ARG;
     if (R > LORA_KV_MAX_REQUESTS || ((long long)max_blocks + 1) * kv->block_tokens > INT32_MAX) return LORA_ERR_TOO_LARGE;
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) ||

@@ -566,7 +566,15 @@ int lora_kv_gather(const lora_kv_cache_t *cache, const int32_t *slots, int T, co
  * max_q_len rows, rows beyond T, or kv_len beyond max_blocks * block_tokens:
  * LORA_DEV_ERR_BAD_LENGTH, its rows left alone.  A block whose table entry is
  * outside the cache is passed over and sets LORA_DEV_ERR_BAD_PAGE.
- * Softmax statistics and sums are fp32.  ws: lora_kv_attend_workspace_size
+ * scale is finite; it may be negative here (lora_prompt_attend refuses that).
+ * Softmax statistics and sums are fp32, with two errors beyond fp32's: a weight
+ * times the step of a value's group is rounded to fp16 (by at most 2^-11 of it)
+ * before it multiplies the codes, and the scores' accumulators carry the codes
+ * offset by 1032 or 72, which leaves a score off by about 2^-24 * 1032 * |scale|
+ * * step * |sum of q| (measured, head_dim 128, steps near 0.3, scale 128^-0.5: 4e-5
+ * for normal queries, 2e-4 where their elements sum to 128; the outputs' error
+ * grows by 1 % over that of the rounding to bf16, by 23 % over that to fp16).
+ * ws: lora_kv_attend_workspace_size
  * bytes, 256-byte aligned, any contents; calls that may overlap on the GPU need
  * workspaces of their own.  q_heads is a multiple of cache->kv_heads, at most
  * LORA_KV_MAX_GROUP times it; R in 1..LORA_KV_MAX_REQUESTS; T * q_heads /

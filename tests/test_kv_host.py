@@ -305,3 +305,10 @@ def test_a_build_with_other_register_counts_is_refused(H):
         with pytest.raises(RuntimeError, match="prompt_kernel"):
             build.check_registers(bad, "prompt_kernel", 168)
     assert set(build.EXACT_REGISTERS) <= {p.rsplit("/", 1)[-1] for p in build.sources()}
+
+
+def test_attend_refuses_a_scale_that_is_not_finite(H):
+    lib = H.load_library()
+    n = H.lora_kv_attend_workspace_size(32, 8, 128, 1)
+    for scale, rc in ((float("nan"), -1), (float("inf"), -1), (-float("inf"), -1), (-1.0, 0), (0.0, 0)):
+        assert lib.lora_kv_attend(rows(H), 0, 32, 0, cache(H), p(), 4, p(), p(), 4, 1, scale, rows(H), None, p(), n, None, None) == rc
