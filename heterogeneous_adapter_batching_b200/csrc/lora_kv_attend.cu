@@ -27,7 +27,9 @@
 // rounded to fp16 (2^-11 relative: an eighth of a bf16 step) after scaling by
 // 32 / sref, sref the largest step so far rounded up to a power of two, so that
 // neither small steps nor small weights leave fp16's range.  Everything else is
-// fp32.
+// fp32; the scores' accumulators carry the offsets of 1032 and 72, so that fp32's
+// last places of a score go with them (lse off by up to 4e-5 for normal queries,
+// 2e-4 where their elements sum to 128).
 //
 // The exponent's reference m is only moved when a score exceeds it by 10 (in
 // powers of two): weights then reach at most 2^10 * 32 in fp16, and the usual
@@ -42,13 +44,15 @@
 // the workspace (at most two per CTA: its first and its last), and a second
 // launch joins those in order.  (Joining by whichever CTA counts itself last
 // saved nothing: 25.4 against 23.1 us for one request, 54.5 against 47.9 us for
-// 48 requests of up to 4 tokens, as the main loop spills more registers.)
+// 48 requests of up to 4 tokens at that time, as the main loop spills more registers.)
 //
 // Measured, 32 / 8 heads of 128, bf16: 32 requests of 8192 tokens 77 us, 3.9 TB/s
-// or 60 % of a copy's rate; 128 requests of 1 to 16384 tokens 62 us (48 %); one of
-// 32749 tokens 23 us.  It is bound by issue slots and latency at 12 warps an SM:
-// 342 instructions a granule and warp, of which 64 products; memory would allow
-// 46 us.  Two granules a warp and step at 3 CTAs an SM: one granule at 4 CTAs takes
+// or 60 % of a copy's rate; 128 requests of 1 to 16384 tokens 62 us (49 %); one of
+// 32749 tokens 23 us.  Latency bounds it: at 12 warps an SM, which the registers
+// allow, warps wait for their own chains (scores, exponentials, transposition,
+// values) and instructions are issued in 57 to 60 % of the cycles; 356
+// instructions a granule, 16 of them products.  Memory would allow 46 us.  Two
+// granules a warp and step at 3 CTAs an SM: one granule at 4 CTAs takes
 // 86 to 90 us, four at 2 CTAs 75 us but 1.5 times as long for short requests.
 // Short requests cost their pieces' beginning and end, about 4 us each and CTA
 // (1024 requests of 64 tokens: 79 us).
@@ -844,9 +848,12 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, con
     if (a.lse && lane == 0) a.lse[(size_t)(s.q0 + qi) * a.hq + head] = ll == 0.f ? -INFINITY : 0.6931471805599453f * (ref + log2f(ll));
 }
 
-// Two column tiles that share one reading of the cache, or one at a time: up to 8 columns there is only one.  Above, two take 110
-// against 116 us (32 requests of 8192, 4 tokens of 4 heads) and 38 against 45 us (16 heads on one), though 43.7 against 41.7 us
-// for 48 ragged requests of up to 4096.
+// Two column tiles that share one reading of the cache, or one at a time: up to 8 columns there is only one.  Above, two take 26.6
+// against 27.9 us (32 requests of 8192, 16 heads on one kv head), 62 against 78 (128 of those), 110 against 116 and 168 against
+// 180 (32 of 8192, 4 and 8 tokens of 32 / 8 heads), but 43.9 against 42.0 us (48 of up to 4096 with 1 to 4 tokens), 42.5 against
+// 37.0 (64 of up to 8192 with 1 to 3) and 65 against 55 (256 of 256 with 4): drafts that do not fill their columns, and short
+// contexts, where 8 warps an SM hide less.  Lengths and rows lie on the device; by the sizes the host has, reading a long cache
+// once is the safer side.
 int tiles_of(int hq, int hkv, int max_q) { return (long long)max_q * (hq / hkv) <= 8 ? 1 : 2; }
 template <int NT>
 constexpr int ctas_per_sm() { return NT == 1 ? 3 : 2; }   // what the registers allow

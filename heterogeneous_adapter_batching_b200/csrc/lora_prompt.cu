@@ -37,11 +37,12 @@
 // and 8-11 own tile 0 and 1.  Waits are bounded (LORA_DEV_ERR_TIMEOUT).  No
 // cluster multicast.
 //
-// Measured, bf16, 32 / 8 heads of 128: one prompt of 8192 tokens 457 to 513 us with
-// the card's power, 1.07 to 1.20 PFLOP/s (a large library product: 1.64); 16 of
-// 128 to 2048 tokens 180 to 200 us; 64 of 128 tokens 51 us; 24 of up to 97 tokens
-// 12 us; one of 16 tokens 8 us.  What bounds long prompts
-// is the tensor pipe's start: a product whose 16 instructions should take 1024
+// Measured, bf16, 32 / 8 heads of 128, among calls of the same kind, which bring the
+// card to its power limit: one prompt of 8192 tokens 525 to 555 us, 0.99 to 1.05
+// PFLOP/s (a large library product: 1.64 in bursts, 1.38 sustained; alone, under a
+// profiler, 498 us); 16 of 128 to 2048 tokens 182 to 209 us; 64 of 128 tokens
+// 46 us; 24 of up to 97 tokens, fp16, heads of 64, 12 us; one of 16 tokens 8 us.
+// What bounds long prompts is the tensor pipe's start: a product whose 16 instructions should take 1024
 // cycles takes about 1450 when it is issued by itself, as the two products of a
 // tile are (one waits for the exponentials, which keep pace).  Products issued by
 // two warps, weights handed over in halves, a quarter of the exponentials as

@@ -573,10 +573,9 @@ int lora_kv_gather(const lora_kv_cache_t *cache, const int32_t *slots, int T, co
  * offset by 1032 or 72, which leaves a score off by about 2^-24 * 1032 * |scale|
  * * step * |sum of q| (measured, head_dim 128, steps near 0.3, scale 128^-0.5: 4e-5
  * for normal queries, 2e-4 where their elements sum to 128; the outputs' error
- * grows by 1 % over that of the rounding to bf16, by 23 % over that to fp16).
- * ws: lora_kv_attend_workspace_size
- * bytes, 256-byte aligned, any contents; calls that may overlap on the GPU need
- * workspaces of their own.  q_heads is a multiple of cache->kv_heads, at most
+ * grows by 1 % over that of the rounding to bf16, by up to 36 % over that to fp16).
+ * ws: lora_kv_attend_workspace_size bytes, 256-byte aligned, any contents;
+ * calls that may overlap on the GPU need workspaces of their own.  q_heads is a multiple of cache->kv_heads, at most
  * LORA_KV_MAX_GROUP times it; R in 1..LORA_KV_MAX_REQUESTS; T * q_heads /
  * kv_heads at most INT32_MAX (lora_prompt_attend too), else
  * LORA_ERR_TOO_LARGE. */
