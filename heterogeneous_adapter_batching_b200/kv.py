@@ -67,7 +67,8 @@ class KVCache:
     several).  A request is a row of the block table: begin() runs lora_kv_layout over the rows' lengths, handing
     out reserved pages; append() and attend() (or prompt_attend()) are the layer's calls; free() gives the pages of
     finished rows back to the pool.  past_len says where the new tokens go: a row whose past has become shorter (drafts
-    that were rejected, a step repeated after an error) fills the blocks it holds again before it takes any.
+    that were rejected, a step repeated after an error) fills the blocks it holds again before it takes any.  block_table
+    and held go together: what clears a row is free().
 
     The calls of a step may be captured in a graph and replayed: every tensor keeps its place, reserve() and free()
     between replays included.  Steps of one KVCache follow one another on one stream (they share its workspace).

@@ -575,10 +575,10 @@ int lora_kv_gather(const lora_kv_cache_t *cache, const int32_t *slots, int T, co
  * for normal queries, 2e-4 where their elements sum to 128; the outputs' error
  * grows by 1 % over that of the rounding to bf16, by up to 36 % over that to fp16).
  * ws: lora_kv_attend_workspace_size bytes, 256-byte aligned, any contents;
- * calls that may overlap on the GPU need workspaces of their own.  q_heads is a multiple of cache->kv_heads, at most
- * LORA_KV_MAX_GROUP times it; R in 1..LORA_KV_MAX_REQUESTS; T * q_heads /
- * kv_heads at most INT32_MAX (lora_prompt_attend too), else
- * LORA_ERR_TOO_LARGE. */
+ * calls that may overlap on the GPU need workspaces of their own.  q_heads is a
+ * multiple of cache->kv_heads, at most LORA_KV_MAX_GROUP times it; R in
+ * 1..LORA_KV_MAX_REQUESTS; T * q_heads / kv_heads at most INT32_MAX
+ * (lora_prompt_attend too), else LORA_ERR_TOO_LARGE. */
 #define LORA_KV_MAX_GROUP 64
 size_t lora_kv_attend_workspace_size(int q_heads, int kv_heads, int head_dim, int max_q_len);
 int lora_kv_attend(const lora_rows_t *q, int T, int q_heads, int dtype, const lora_kv_cache_t *cache,
