@@ -117,13 +117,13 @@ __device__ __forceinline__ uint32_t range_of(const uint32_t (&u)[4]) {
     return Pair<D>::less(__byte_perm(l, g, 0x5410), __byte_perm(l, g, 0x7632));
 }
 
-// x - y rounded, and what the rounding left out.
+// x - y rounded, and what the rounding left out (Knuth's two-sum).
 __device__ __forceinline__ double minus(double x, double y, double &rest) {
     const double d = x - y, b = d - x;
     rest = (x - (d - b)) - (y + b);
     return d;
 }
-// (x - y) / 15 rounded once to fp16.
+// (x - y) / 15 rounded once to fp16: through a quotient rounded to odd (Boldo and Melquiond's method against double rounding).
 __device__ __forceinline__ __half fifteenth(double x, double y) {
     double rest;
     const double diff = minus(x, y, rest);

@@ -256,7 +256,7 @@ def test_layout_of_held_blocks_refusals(H):
 
     def call(held=p(4096), held_out=p(8192), past=p(), kv=p(12288)):
         return lib.lora_kv_layout_held(past, p(256), None, 4, 0, 16, p(512), 4, p(1024), 10, p(2048), p(2304), kv, None, None, None,
-                                       p(3072), held, held_out, None, None)
+                                       p(3328), held, held_out, None, None)
 
     assert call(held=None) == -1 and call(held_out=None) == -1 and call(past=None) == -1
     assert call(held_out=p(4096)) == -1 and call(held_out=p(4096 + 12)) == -1      # not in place
