@@ -108,7 +108,7 @@ __device__ __forceinline__ Req load_req(const AttendArgs &a, int r, int G, bool 
     if (bad || q1 == q.q0) q.nq = 0;
     q.tiles = (q.nq * G + NC - 1) / NC;
     constexpr int tokens = ROUND * LORA_KV_GRANULE;
-    q.rounds = q.len <= 0 ? 1 : (q.len + tokens - 1) / tokens;
+    q.rounds = q.len <= 0 ? 1 : (q.len - 1) / tokens + 1;   // lengths reach 2^31 - 17
     return q;
 }
 
@@ -155,7 +155,7 @@ struct Walk {
     // granules of the piece: [g0, g1)
     __device__ __forceinline__ int g0() const { return round * ROUND; }
     __device__ __forceinline__ int g1() const {
-        const int all = q.len <= 0 ? 0 : (q.len + LORA_KV_GRANULE - 1) / LORA_KV_GRANULE;
+        const int all = q.len <= 0 ? 0 : (q.len - 1) / LORA_KV_GRANULE + 1;
         return min(all, (round + n) * ROUND);
     }
 };

@@ -101,7 +101,8 @@ class KVCache:
                               device=dev)
 
     def reserve(self, n: int) -> None:
-        """Take n pages of the pool for the steps to come.  Synchronises the device."""
+        """Take n pages of the pool for the steps to come.  Synchronises the device.  What is left of them when the object
+        goes, free_list[head:], goes back through lora_pool_free_page_list."""
         torch.cuda.synchronize(self.device)
         ids = B.lora_pool_alloc_pages(self.pool, n)
         kept = self.free_list[int(self.head.item()):]

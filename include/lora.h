@@ -597,6 +597,7 @@ int lora_kv_attend(const lora_rows_t *q, int T, int q_heads, int dtype, const lo
  *   finite and not negative; lse [Tq][q_heads] fp32 or NULL.  cu_q, cu_k
  *   [R+1] int32 on the device, not decreasing, within [0, Tq] and [0, Tk]: a
  *   request that is not sets LORA_DEV_ERR_BAD_LENGTH and its rows are left alone.
+ *   R in 1..LORA_KV_MAX_REQUESTS.
  * Rows outside [cu_q[0], cu_q[R]) are left alone.  A row that attends to nothing
  * gets out = 0, lse = -inf.  Other requests' rows and rows behind the last one
  * do not affect a request, whatever they hold (NaN included); within a request,

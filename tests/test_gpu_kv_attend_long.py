@@ -228,3 +228,35 @@ def test_the_check_sees_single_tokens():
     twice[:, 5] *= 2
     turned[1000:1016] = v[1000:1016].flip(0)
     assert refused(gone, v) and refused(twice, v) and refused(scaled, v) and refused(p, turned)
+
+
+def test_the_longest_context_that_is_taken(H):
+    """2^31 - 32 tokens in blocks of 16, every entry of the table the same page: as 16 tokens, each 134217726 times.
+
+    A warp adds up 134217726 / 1776 = 75572 granules: accumulations of 2^-23 each come to 0.9 %, the two sums of weights a granule
+    of 2^-24 each to 0.9 % more."""
+    n = ((2 ** 31 - 1) // 16 - 1) * 16
+    c = Contexts(2, [16], 1, 64, 16)
+    table = torch.full((1, n // 16), int(c.table[0, 0]), dtype=torch.int32, device="cuda")
+    q = queries(1, 1, 4, 64, FP)
+    out, lse, err = torch.full_like(q, 7.0), torch.full((1, 4), 7.0, device="cuda"), i32([0])
+    ws = torch.empty(H.lora_kv_attend_workspace_size(4, 1, 64, 1), dtype=torch.uint8, device="cuda")
+    H.lora_kv_attend(q, c.pages, 16, 1, table, i32([0, 1]), i32([n]), 1, 0.125, out, ws, lse=lse, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    k, v, _ = c.values(0, 0)
+    s = (q[0].double() @ k.T) * 0.125
+    o, l = torch.softmax(s, -1) @ v, torch.logsumexp(s, -1) + math.log(n // 16)
+    assert ((out[0].double() - o).norm(dim=-1) <= 2.0 ** -5 * (torch.softmax(s, -1) @ v.abs()).norm(dim=-1)).all()
+    assert ((lse[0].double() - l).abs() <= 2.0 ** -5).all()
+
+
+def test_as_many_requests_as_a_call_takes(H):
+    r = np.random.default_rng(8)
+    lens = [int(x) for x in r.integers(0, 50, 4096)]
+    c = Contexts(4, lens, 1, 64, 16)
+    q_lens = [min(int(x), n) for x, n in zip(r.integers(0, 3, 4096), lens)]
+    q = queries(5, sum(q_lens), 4, 64, FP)
+    out, lse, err = run(H, c, q, q_lens, 2, 0.125)
+    assert err == 0
+    check(c, q, q_lens, 0.125, out, lse, FP)

@@ -75,3 +75,15 @@ def test_rows_by_their_norm(H, dtype, hq, hk, dim, q_lens, past):
         outs.append((out, lse))
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
     check(q, k, v, [int(x) for x in cu_q], [int(x) for x in cu_k], scale, out, lse, dtype)
+
+
+def test_as_many_requests_as_a_call_takes(H):
+    n = np.random.default_rng(6).integers(0, 12, 4096)
+    n[4000] = 700
+    cu = [int(x) for x in np.r_[0, np.cumsum(n)]]
+    q, k, v = (rows(i, cu[-1], m, 64, FP) for i, m in ((1, 2), (2, 1), (3, 1)))
+    out, lse, err = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda"), i32([0])
+    H.lora_prompt_attend(q, k, v, i32(cu), i32(cu), 0.125, out, lse=lse, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check(q, k, v, cu, cu, 0.125, out, lse, FP)
